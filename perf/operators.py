@@ -262,8 +262,8 @@ def prepare(c, seed):
             st["cache"] = ispa.kvq_desc(Hkv, d, c["page"], st["pages"], fmt)
         if c["op"] in ("attn", "prompt"):
             st["attn"] = ispa.attn_seq_desc(B, H, Hkv, d, code, code, causal=c["causal"])
-        if c["op"] == "attn":
-            st["ws"] = torch.empty(ispa.ispa_attn_kvq_workspace_bytes(st["attn"], st["cache"]), dtype=torch.uint8, device="cuda")
+            size = ispa.ispa_attn_kvq_workspace_bytes(st["attn"], st["cache"]) if c["op"] == "attn" else ispa.ispa_attn_prompt_workspace_bytes(st["attn"])
+            st["ws"] = torch.empty(size, dtype=torch.uint8, device="cuda")
     return st
 
 
@@ -279,9 +279,10 @@ def run(st):
                                seq_begin=st["begin"])
         if c["op"] == "attn":
             ispa.ispa_attn_kvq(st["attn"], st["cache"], st["q"], st["kvq"], st["table"], st["lens"], st["cu_new"],
-                               st["max_new"], st["o"], st["lse"], workspace=st["ws"])
+                               st["o"], st["lse"], workspace=st["ws"])
         if c["op"] == "prompt":
-            ispa.ispa_attn_prompt(st["attn"], st["q"], st["k"], st["v"], st["cu_new"], st["cu_k"], st["o"], st["lse"])
+            ispa.ispa_attn_prompt(st["attn"], st["q"], st["k"], st["v"], st["cu_new"], st["cu_k"], st["o"], st["lse"],
+                                  workspace=st["ws"])
     else:
         if c["op"] == "write":
             store(c, st, st["cu_new"], st["begin"], st["n"], st["k"], 0)
