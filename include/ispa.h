@@ -26,6 +26,8 @@
  *   - Conditions found on the device (a non positive-definite matrix, a bounded
  *     wait that timed out) are recorded in a per-device error word and are
  *     reported by ispa_check_device_error(), which synchronises the stream.
+ *     The sequence calls record lengths, row bounds and page numbers found out
+ *     of range there as ISPA_ERR_INVALID_ARG (detail: the sequence's index).
  *   - Tensor pointers must be 16-byte aligned.  Row-major, C-contiguous layouts.
  *   - ispa_last_error() returns a thread-local description of the last failure.
  *   - Matrices act on row vectors: y = a W with W of shape [D_in, D_out].
@@ -52,7 +54,8 @@ typedef enum {
   ISPA_ERR_TIMEOUT = 5      /* a bounded device-side wait gave up                */
 } ispa_status;
 
-typedef enum { ISPA_F32 = 0, ISPA_BF16 = 1 } ispa_dtype;
+/* ISPA_F16 is taken by the sequence calls (ispa_kvq_*, ispa_attn_kvq, ispa_attn_prompt) only. */
+typedef enum { ISPA_F32 = 0, ISPA_BF16 = 1, ISPA_F16 = 2 } ispa_dtype;
 
 /* 8-bit format of the W8A8 projection (one byte per value). */
 typedef enum {
@@ -84,7 +87,8 @@ uint64_t ispa_launch_count(void);
  * device.  Returns ISPA_OK, ISPA_ERR_NOT_SPD or ISPA_ERR_TIMEOUT (or
  * ISPA_ERR_CUDA if the synchronisation itself failed).  `detail` (optional,
  * host) receives the code's argument: the 1-based failing pivot for NOT_SPD,
- * the kernel's wait-site id for TIMEOUT.
+ * the kernel's wait-site id for TIMEOUT, the sequence's index for the
+ * ISPA_ERR_INVALID_ARG of a sequence call.
  */
 ispa_status ispa_check_device_error(ispa_stream_t stream, int *detail);
 
@@ -549,6 +553,143 @@ ispa_status ispa_attn_local_proj_q8(const ispa_attn_desc *desc, const void *q, c
                                     const void *v, const void *qT, const float *sw,
                                     ispa_q8_format fmt, int Dout, void *y, ispa_dtype y_dtype,
                                     void *workspace, size_t workspace_bytes, ispa_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Sequences: a quantised paged KV cache and attention over packed prompts    */
+/* ------------------------------------------------------------------------- */
+/*
+ * The calls below serve token sequences of different lengths beside the frame
+ * layouts above: prompts packed one behind the other, and a cache whose tokens
+ * lie in fixed-size pages, quantised to 8 or 4 bits per value when they are
+ * written (cache compression by number format, next to the absorption that
+ * drops tokens; a token evicted by the caller is one whose page leaves the
+ * block table).  Their outputs (O and its log-sum-exp) have the layout of the
+ * other attention calls, so ispa_lse_merge combines them with any other group.
+ *
+ * Arguments they share, all device arrays of int32:
+ *   cu_*         [B + 1], non-decreasing: sequence b owns the packed rows
+ *                [cu[b], cu[b+1]).  Rows from cu[B] on (padding) are neither
+ *                read nor written.  A sequence may be empty.
+ *   block_table  [B, max_pages]: page i of sequence b holds its positions
+ *                [i * page_tokens, (i + 1) * page_tokens).  Entries past a
+ *                sequence's length are not read (any value).  A page belongs
+ *                to one sequence, or is shared by sequences that only read it.
+ *   seq_lens     [B]: tokens of sequence b in the cache.
+ * Values out of range (a cu outside [0, T], a length above max_pages *
+ * page_tokens, a page outside [0, n_pages)) touch no memory out of bounds:
+ * bounds are clamped, a token without a valid page is skipped (written
+ * nowhere, read as zeros, left out of an attention), and the device error word
+ * records ISPA_ERR_INVALID_ARG with the sequence's index.
+ *
+ * K, V and Q rows may be strided: row t of k starts at k + t * k_stride
+ * elements (k_stride >= H_kv * head_dim, a multiple of 8), with the row's
+ * heads back to back, so that they can be slices of a fused projection.
+ * Outputs are contiguous.  head_dim is 64 or 128.
+ */
+
+/* How the cache stores a row (one token of one head of K or of V, d values x). */
+typedef enum {
+  ISPA_KVQ_E4M3 = 0, /* d codes e4m3(448 x / amax), nearest even; scale amax / 448       */
+  ISPA_KVQ_INT8 = 1, /* d codes rint(127 x / amax) in [-127, 127]; scale amax / 127       */
+  ISPA_KVQ_INT4 = 2  /* d / 2 bytes: per 32 channels a factor g = e4m3(448 amax_32 / amax),
+                        n = rint(3136 x / (amax g)) in [-7, 7], stored as n + 8 (channel 2j
+                        in the low nibble of byte j); scale record of 8 bytes: the fp32
+                        s = amax / 3136, then the d / 32 factors g, then zeros; x ~ n s g  */
+} ispa_kvq_format;
+
+typedef struct {
+  int H_kv;             /* heads of K and V                                          */
+  int head_dim;         /* 64 or 128                                                 */
+  int page_tokens;      /* tokens per page: 16, 32, 64, 128 or 256                   */
+  int n_pages;          /* pages of the buffer                                       */
+  ispa_kvq_format fmt;
+} ispa_kvq_desc;
+
+/*
+ * The cache of one layer: one caller-owned buffer of ispa_kvq_bytes(desc)
+ * bytes (0 for an invalid desc), 16-byte aligned, of four sections, each
+ * [n_pages, H_kv, page_tokens, row bytes] and starting on a multiple of 256
+ * bytes: codes of K, codes of V, scale records of K, scale records of V.  Row
+ * bytes: codes d (e4m3, int8) or d / 2 (int4); records 4 or 8.  It needs no
+ * initialisation: rows that no sequence's length covers are not read.
+ *
+ * ispa_kvq_write quantises the T packed rows of k and v (in_dtype ISPA_BF16 or
+ * ISPA_F16, finite values): row i of sequence b goes to position
+ * seq_lens[b] - (cu_new[b+1] - cu_new[b]) + i, that is, seq_lens counts the new
+ * tokens already.  The quotients above are decided exactly (as in real
+ * arithmetic, ties to even); a row whose amax is below 2^-96 is stored as
+ * zeros.  Two rows written to one place (a page shared by two writers) leave
+ * that place with a mixture of both.  Asynchronous; T == 0 is a no-op.
+ *
+ * ispa_kvq_read is the inverse: row i of sequence b's output rows
+ * [cu_out[b], cu_out[b+1]) is position seq_begin[b] + i (seq_begin NULL: 0) of
+ * its cache, as code * scale in fp32 (int4: n * (s * g)) rounded once to
+ * out_dtype (ISPA_BF16 or ISPA_F16).  k_out, v_out [T, H_kv, d].
+ */
+size_t ispa_kvq_bytes(const ispa_kvq_desc *desc);
+ispa_status ispa_kvq_write(const ispa_kvq_desc *desc, int B, int T, const int *block_table, int max_pages,
+                           const int *seq_lens, const int *cu_new, const void *k, long long k_stride, const void *v,
+                           long long v_stride, ispa_dtype in_dtype, void *kvq, ispa_stream_t stream);
+ispa_status ispa_kvq_read(const ispa_kvq_desc *desc, int B, int T, const int *block_table, int max_pages,
+                          const int *seq_begin, const int *cu_out, const void *kvq, void *k_out, void *v_out,
+                          ispa_dtype out_dtype, ispa_stream_t stream);
+
+/* Attention over sequences: H query heads share H_kv heads of K and V, query
+ * head h reading head h / (H / H_kv). */
+typedef struct {
+  int B;                /* sequences                                                 */
+  int H, H_kv;          /* H a multiple of H_kv, H / H_kv <= 128                     */
+  int head_dim;         /* 64 or 128                                                 */
+  ispa_dtype in_dtype;  /* ISPA_BF16 or ISPA_F16: Q (and K, V of a prompt)           */
+  ispa_dtype out_dtype; /* O: in_dtype or ISPA_F32                                   */
+  int causal;           /* 1: query i of n sees keys j <= len - n + i; 0: every key  */
+  float softmax_scale;  /* <= 0 selects 1/sqrt(head_dim)                             */
+} ispa_attn_seq_desc;
+
+/*
+ * Attention of the newest tokens of each sequence over its cache, which is
+ * read as it lies in the pages (nothing is dequantised to memory): the
+ * decoding step (one query token per sequence), or a few pending or drafted
+ * tokens.  Sequence b's queries are the rows [cu_q[b], cu_q[b+1]) of q
+ * [T, H, d], its keys the first seq_lens[b] tokens of its cache; with causal,
+ * the queries are its last tokens (already written).  Any number of query
+ * tokens is taken; the cache is read once per 16 rows of tokens * (H / H_kv).
+ *   o    [T, H, d] out_dtype, lse [T, H] fp32 or NULL.  A query that sees no
+ *        key gives O = 0, lse = -inf.
+ *   Arithmetic: q in fp16 scaled by a power of two per row (exact for entries
+ *   above 2^-29 of the row's largest), codes exactly in fp16, products
+ *   accumulated in fp32; softmax statistics in fp32; the weights, times the
+ *   V scale, enter the second product in fp16 (11 significant bits).
+ *   workspace >= ispa_attn_kvq_workspace_bytes(...), 16-byte aligned: partial
+ *   results of sequences that several SMs share.  Calls (or captured graphs)
+ *   that may run at the same time need one each.  The same inputs give the
+ *   same bits.
+ */
+size_t ispa_attn_kvq_workspace_bytes(const ispa_attn_seq_desc *desc, const ispa_kvq_desc *cache);
+ispa_status ispa_attn_kvq(const ispa_attn_seq_desc *desc, const ispa_kvq_desc *cache, int T, const int *cu_q,
+                          const int *block_table, int max_pages, const int *seq_lens, const void *q,
+                          long long q_stride, const void *kvq, void *o, float *lse, void *workspace,
+                          size_t workspace_bytes, ispa_stream_t stream);
+
+/*
+ * Attention of whole prompts: sequence b's queries are the rows
+ * [cu_q[b], cu_q[b+1]) of q [Tq, H, d], its keys and values the rows
+ * [cu_k[b], cu_k[b+1]) of k and v [Tk, H_kv, d].  With fewer queries than keys
+ * the queries are the last ones (a chunk after a prefix, e.g. one brought back
+ * by ispa_kvq_read); with causal and more queries than keys the first queries
+ * see nothing.  The rows of one sequence must hold finite values; those of
+ * others, and padding, do not matter to it.
+ *   o    [Tq, H, d] out_dtype, lse [Tq, H] fp32 or NULL.  A query that sees no
+ *        key gives O = 0, lse = -inf.
+ *   tcgen05 tensor cores, fp32 accumulation and statistics; the softmax
+ *   weights enter the second product in in_dtype.
+ *   workspace >= ispa_attn_prompt_workspace_bytes(desc), as for ispa_attn_kvq.
+ */
+size_t ispa_attn_prompt_workspace_bytes(const ispa_attn_seq_desc *desc);
+ispa_status ispa_attn_prompt(const ispa_attn_seq_desc *desc, int Tq, int Tk, const int *cu_q, const int *cu_k,
+                             const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
+                             long long v_stride, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                             ispa_stream_t stream);
 
 #ifdef __cplusplus
 }

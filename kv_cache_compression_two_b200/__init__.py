@@ -21,10 +21,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libispa.so")
 
 ISPA_OK, ISPA_ERR_INVALID_ARG, ISPA_ERR_UNSUPPORTED, ISPA_ERR_CUDA, ISPA_ERR_NOT_SPD, ISPA_ERR_TIMEOUT = range(6)
-ISPA_F32, ISPA_BF16 = 0, 1
+ISPA_F32, ISPA_BF16, ISPA_F16 = 0, 1, 2
 ISPA_PREC_TF32, ISPA_PREC_F32 = 0, 1
 ISPA_Q8_E4M3, ISPA_Q8_INT8 = 0, 1
 ISPA_V_PLAIN, ISPA_V_F16_PREPARED, ISPA_KV_E4M3_PREPARED = 0, 1, 2
+ISPA_KVQ_E4M3, ISPA_KVQ_INT8, ISPA_KVQ_INT4 = 0, 1, 2
 
 STATUS_NAMES = {0: "ISPA_OK", 1: "ISPA_ERR_INVALID_ARG", 2: "ISPA_ERR_UNSUPPORTED", 3: "ISPA_ERR_CUDA",
                 4: "ISPA_ERR_NOT_SPD", 5: "ISPA_ERR_TIMEOUT"}
@@ -38,7 +39,8 @@ EXPORTED = ("ispa_version", "ispa_last_error", "ispa_launch_count", "ispa_check_
             "ispa_quantize_weight", "ispa_gemm_q8", "ispa_gemm_bf16", "ispa_attn_local_proj_q8_workspace_bytes",
             "ispa_attn_local_proj_q8", "ispa_warmup_fused_workspace_bytes", "ispa_warmup_fused",
             "ispa_v16_bytes", "ispa_v16_prepare", "ispa_absorb_error_workspace_bytes", "ispa_absorb_error",
-            "ispa_kv8_bytes", "ispa_kv8_prepare")
+            "ispa_kv8_bytes", "ispa_kv8_prepare", "ispa_kvq_bytes", "ispa_kvq_write", "ispa_kvq_read",
+            "ispa_attn_kvq_workspace_bytes", "ispa_attn_kvq", "ispa_attn_prompt_workspace_bytes", "ispa_attn_prompt")
 RIDGE_NOALLOC_MAX_D = RIDGE_NOALLOC_MAX_DOUT = 1024
 
 
@@ -71,8 +73,31 @@ def prepared(desc: AttnDesc, layout: int = ISPA_V_F16_PREPARED) -> AttnDesc:
     return d
 
 
+class KvqDesc(ctypes.Structure):
+    _fields_ = [("H_kv", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("fmt", ctypes.c_int)]
+
+
+class AttnSeqDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("causal", ctypes.c_int),
+                ("softmax_scale", ctypes.c_float)]
+
+
+def kvq_desc(H_kv: int, head_dim: int, page_tokens: int, n_pages: int, fmt: int) -> KvqDesc:
+    """The layout of one layer's quantised paged cache (fmt: ISPA_KVQ_E4M3, _INT8 or _INT4)."""
+    return KvqDesc(H_kv, head_dim, page_tokens, n_pages, fmt)
+
+
+def attn_seq_desc(B: int, H: int, H_kv: int, head_dim: int, in_dtype: int, out_dtype: int, causal: bool = True,
+                  softmax_scale: float = 0.0) -> AttnSeqDesc:
+    """An attention over B sequences with H query heads on H_kv K/V heads."""
+    return AttnSeqDesc(B, H, H_kv, head_dim, in_dtype, out_dtype, int(bool(causal)), softmax_scale)
+
+
 _lib = None
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 def lib() -> ctypes.CDLL:
@@ -122,6 +147,16 @@ def lib() -> ctypes.CDLL:
         "ispa_kv8_prepare": (_ci, [ctypes.POINTER(AttnDesc), _vp, _vp, _ci, _ci, _vp, _vp]),
         "ispa_absorb_error": (_ci, [_ci, _ci, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
         "ispa_v16_prepare": (_ci, [ctypes.POINTER(AttnDesc), _vp, _ci, _ci, _vp, _vp]),
+        "ispa_kvq_bytes": (_sz, [ctypes.POINTER(KvqDesc)]),
+        "ispa_kvq_write": (_ci, [ctypes.POINTER(KvqDesc), _ci, _ci, _vp, _ci, _vp, _vp, _vp, _ll, _vp, _ll, _ci, _vp,
+                                 _vp]),
+        "ispa_kvq_read": (_ci, [ctypes.POINTER(KvqDesc), _ci, _ci, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _ci, _vp]),
+        "ispa_attn_kvq_workspace_bytes": (_sz, [ctypes.POINTER(AttnSeqDesc), ctypes.POINTER(KvqDesc)]),
+        "ispa_attn_kvq": (_ci, [ctypes.POINTER(AttnSeqDesc), ctypes.POINTER(KvqDesc), _ci, _vp, _vp, _ci, _vp, _vp,
+                                _ll, _vp, _vp, _vp, _vp, _sz, _vp]),
+        "ispa_attn_prompt_workspace_bytes": (_sz, [ctypes.POINTER(AttnSeqDesc)]),
+        "ispa_attn_prompt": (_ci, [ctypes.POINTER(AttnSeqDesc), _ci, _ci, _vp, _vp, _vp, _ll, _vp, _ll, _vp, _ll, _vp,
+                                   _vp, _vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -362,6 +397,138 @@ ISPA_SELFTEST_SITE = 999
 
 def ispa_selftest_wait_timeout(wait_ns: int, stream=None) -> None:
     _check(lib().ispa_selftest_wait_timeout(int(wait_ns), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Sequences: the quantised paged cache and attention over packed prompts
+# ---------------------------------------------------------------------------
+class _Seq:
+    """One sequence call's view of its tensors: all on the current device, contents and shapes checked."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.dev = torch.cuda.current_device()
+        self.ints, self.bytes_, self.f32 = torch.int32, torch.uint8, torch.float32
+        self.code = {torch.bfloat16: ISPA_BF16, torch.float16: ISPA_F16, torch.float32: ISPA_F32}
+
+    def ptr(self, x, name, dtype, shape):
+        """A contiguous tensor of this dtype; shape entries that are None may have any size."""
+        if not isinstance(x, self.torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if x.dtype != dtype:
+            raise ValueError(f"{name}: dtype {x.dtype}, expected {dtype}")
+        if x.get_device() != self.dev:
+            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{self.dev}")
+        have = x.shape
+        if len(have) != len(shape) or any(w is not None and w != h for w, h in zip(shape, have)):
+            raise ValueError(f"{name}: shape {tuple(have)}, expected {shape}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        return x.data_ptr()
+
+    def rows(self, x, name, heads, d, dtype=None):
+        """Packed rows [T, heads, d] whose tokens may be strided: (pointer, T, stride, dtype code)."""
+        if not isinstance(x, self.torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        code = self.code.get(x.dtype)
+        if code is None or code == ISPA_F32 or (dtype is not None and code != dtype):
+            raise ValueError(f"{name}: dtype {x.dtype} does not fit the call")
+        if x.get_device() != self.dev:
+            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{self.dev}")
+        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d:
+            raise ValueError(f"{name}: shape {tuple(x.shape)}, expected [T, {heads}, {d}]")
+        T, stride = x.shape[0], x.stride()
+        if T <= 1:
+            step = heads * d
+        else:
+            step = stride[0]
+        if T and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+            raise ValueError(f"{name}: a row's heads must lie back to back")
+        return x.data_ptr(), T, step, code
+
+    def cache(self, desc, kvq, table, B):
+        need = ispa_kvq_bytes(desc)
+        if need == 0:
+            raise ValueError("desc: not a valid cache layout")
+        if isinstance(kvq, self.torch.Tensor) and kvq.numel() < need:
+            raise ValueError(f"kvq: {kvq.numel()} bytes, the layout needs {need}")
+        return self.ptr(kvq, "kvq", self.bytes_, (None,)), self.ptr(table, "block_table", self.ints, (B, None))
+
+
+def ispa_kvq_bytes(desc: KvqDesc) -> int:
+    return int(lib().ispa_kvq_bytes(ctypes.byref(desc)))
+
+
+def ispa_kvq_write(desc: KvqDesc, k, v, block_table, seq_lens, cu_new, kvq, stream=None) -> None:
+    """Quantises the packed rows k, v [T, H_kv, d] into the cache (seq_lens counts them already)."""
+    s = _Seq()
+    B = seq_lens.shape[0]
+    kp, T, ks, dt = s.rows(k, "k", desc.H_kv, desc.head_dim)
+    vp, Tv, vs, _ = s.rows(v, "v", desc.H_kv, desc.head_dim, dt)
+    if T != Tv:
+        raise ValueError(f"k has {T} rows, v {Tv}")
+    cp, tp = s.cache(desc, kvq, block_table, B)
+    _check(lib().ispa_kvq_write(ctypes.byref(desc), B, T, tp, block_table.shape[1],
+                                s.ptr(seq_lens, "seq_lens", s.ints, (B,)), s.ptr(cu_new, "cu_new", s.ints, (B + 1,)),
+                                kp, ks, vp, vs, dt, cp, _stream(stream)))
+
+
+def ispa_kvq_read(desc: KvqDesc, kvq, block_table, cu_out, k_out, v_out, seq_begin=None, stream=None) -> None:
+    """Reads positions seq_begin[b] + i of each sequence back into the packed k_out, v_out [T, H_kv, d]."""
+    s = _Seq()
+    B, T = cu_out.shape[0] - 1, k_out.shape[0]
+    shape = (T, desc.H_kv, desc.head_dim)
+    cp, tp = s.cache(desc, kvq, block_table, B)
+    begin = None if seq_begin is None else s.ptr(seq_begin, "seq_begin", s.ints, (B,))
+    _check(lib().ispa_kvq_read(ctypes.byref(desc), B, T, tp, block_table.shape[1], begin,
+                               s.ptr(cu_out, "cu_out", s.ints, (B + 1,)), cp, s.ptr(k_out, "k_out", k_out.dtype, shape),
+                               s.ptr(v_out, "v_out", k_out.dtype, shape), s.code.get(k_out.dtype, -1),
+                               _stream(stream)))
+
+
+def ispa_attn_kvq_workspace_bytes(desc: AttnSeqDesc, cache: KvqDesc) -> int:
+    return int(lib().ispa_attn_kvq_workspace_bytes(ctypes.byref(desc), ctypes.byref(cache)))
+
+
+def _seq_outputs(s, desc, T, o, lse, workspace):
+    out = s.torch.float32 if desc.out_dtype == ISPA_F32 else (
+        s.torch.bfloat16 if desc.out_dtype == ISPA_BF16 else s.torch.float16)
+    op = s.ptr(o, "o", out, (T, desc.H, desc.head_dim))
+    lp = None if lse is None else s.ptr(lse, "lse", s.f32, (T, desc.H))
+    wp = s.ptr(workspace, "workspace", s.bytes_, (None,))
+    return op, lp, wp, workspace.shape[0]
+
+
+def ispa_attn_kvq(desc: AttnSeqDesc, cache: KvqDesc, q, kvq, block_table, seq_lens, cu_q, o, lse=None, workspace=None,
+                  stream=None) -> None:
+    """Attention of the packed queries q [T, H, d] over each sequence's quantised cache."""
+    s = _Seq()
+    qp, T, qs, _ = s.rows(q, "q", desc.H, desc.head_dim, desc.in_dtype)
+    cp, tp = s.cache(cache, kvq, block_table, desc.B)
+    op, lp, wp, wn = _seq_outputs(s, desc, T, o, lse, workspace)
+    _check(lib().ispa_attn_kvq(ctypes.byref(desc), ctypes.byref(cache), T,
+                               s.ptr(cu_q, "cu_q", s.ints, (desc.B + 1,)), tp, block_table.shape[1],
+                               s.ptr(seq_lens, "seq_lens", s.ints, (desc.B,)), qp, qs, cp, op, lp, wp, wn,
+                               _stream(stream)))
+
+
+def ispa_attn_prompt_workspace_bytes(desc: AttnSeqDesc) -> int:
+    return int(lib().ispa_attn_prompt_workspace_bytes(ctypes.byref(desc)))
+
+
+def ispa_attn_prompt(desc: AttnSeqDesc, q, k, v, cu_q, cu_k, o, lse=None, workspace=None, stream=None) -> None:
+    """Attention of packed prompts: q [Tq, H, d] over k, v [Tk, H_kv, d]."""
+    s = _Seq()
+    qp, Tq, qs, _ = s.rows(q, "q", desc.H, desc.head_dim, desc.in_dtype)
+    kp, Tk, ks, _ = s.rows(k, "k", desc.H_kv, desc.head_dim, desc.in_dtype)
+    vp, Tv, vs, _ = s.rows(v, "v", desc.H_kv, desc.head_dim, desc.in_dtype)
+    if Tk != Tv:
+        raise ValueError(f"k has {Tk} rows, v {Tv}")
+    op, lp, wp, wn = _seq_outputs(s, desc, Tq, o, lse, workspace)
+    _check(lib().ispa_attn_prompt(ctypes.byref(desc), Tq, Tk, s.ptr(cu_q, "cu_q", s.ints, (desc.B + 1,)),
+                                  s.ptr(cu_k, "cu_k", s.ints, (desc.B + 1,)), qp, qs, kp, ks, vp, vs, op, lp, wp, wn,
+                                  _stream(stream)))
 
 
 lib()

@@ -276,6 +276,8 @@ ispa_status ispa_check_device_error(ispa_stream_t stream, int *detail) {
   if (detail) *detail = host[1];
   if (host[0] == ISPA_ERR_NOT_SPD) return fail(ISPA_ERR_NOT_SPD, "G + lambda I is not positive definite (pivot %d)", host[1]);
   if (host[0] == ISPA_ERR_TIMEOUT) return fail(ISPA_ERR_TIMEOUT, "device-side wait timed out (site %d)", host[1]);
+  if (host[0] == ISPA_ERR_INVALID_ARG)
+    return fail(ISPA_ERR_INVALID_ARG, "a length, row bound or page number of sequence %d is out of range", host[1]);
   if (host[0] != 0) return fail(ISPA_ERR_CUDA, "device error code %d", host[0]);
   return ISPA_OK;
 }

@@ -1,0 +1,729 @@
+// attn_prompt.cu -- attention of packed prompts on tcgen05 tensor cores (bf16 or fp16, d = 64 or 128).
+//
+// A persistent CTA per SM walks an even stretch of the call's work (seq.cuh);
+// an item is a pair of 128-row query tiles of one K/V head, a step one
+// 128-key tile for both.  The rows of a tile are tokens x the H / H_kv heads
+// that share the K/V head (row = token * group + head), so grouped heads share
+// every K/V tile, short sequences fill the tiles better, and a causal tile's
+// diagonal is 128 / group tokens wide.
+//
+// Warps (384 threads):
+//   0      TMA producer: the pair's Q tiles, then K_0, V_0, K_1, V_1, ... through
+//          one ring of stages
+//   1      TMEM allocator and MMA issuer (whole warp; one lane issues)
+//   2, 3   idle
+//   4-7    softmax and output of tile A, one row per thread (TMEM lane = row)
+//   8-11   the same for tile B
+// TMEM: S of A [0,128), S of B [128,256), O of A [256,256+d), O of B [384,384+d).
+// P overwrites the first 64 columns of its S.  The issuer's order is
+//   S_A0 S_B0 | PV_A0 S_A1 | PV_B0 S_B1 | PV_A1 S_A2 | ...
+// so while one warpgroup works on its scores the tensor cores run the other
+// tile's two products: the softmax's latency chain, which bounds a kernel with
+// one tile in flight, is hidden behind the other tile.  Q and K come from
+// shared memory (S is SS, PV is TS): measured by itself the pair S + PV of a
+// 128 x 128 x 128 tile takes 1204 cycles against 1024 at the nominal rate, and
+// keeping Q in TMEM instead would leave no room for the second tile.
+//
+// Ordering (MMAs of one thread execute in order; a commit fires when all
+// earlier ones have completed): S_{j+1} is issued after PV_j of the same tile,
+// so it may overwrite P_j, and s_full(j + 1) says that O holds PV_0..PV_j: a
+// softmax warp that has seen it may rescale O without a further wait, PV_{j+1}
+// being held back by p_full(j + 1).  The last PV of an item commits o_final;
+// the next item's first PV overwrites O after the p_full that the same
+// warpgroup publishes behind its reading of O.
+//
+// Keys: a tile past the end of its sequence holds rows of the next one, or
+// zeros.  Scores there are replaced by -inf; in the second product only the
+// 16-key steps that hold a visible key are issued, and the issuing warp zeroes
+// the rows that remain of the last one (0 * Inf would not be 0).
+#include <algorithm>
+#include <type_traits>
+
+#include "internal.h"
+#include "seq.cuh"
+
+namespace ispa {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;
+constexpr int kBox = 128 * 128;  // bytes of 128 rows x 64 columns
+constexpr int kMinPart = 4;
+constexpr float kThreshold = 8.0f;  // the reference maximum moves when passed by more than this (log2)
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct PromptParams {
+  int B, H, H_kv, G, TQ;  // G = H / H_kv heads per K/V head, TQ = 128 / G tokens per tile
+  int Tq, Tk, causal, nc;
+  float scale_log2;
+  const int *cu_q, *cu_k;
+  void *o;
+  float *lse;
+  float *part;     // [2 nc][2 tiles][m 128 | l 128 | O as float4 [d / 4][128 rows]]
+  PartMeta *meta;  // [2 nc]
+  DevErr err;
+};
+
+template <int D>
+constexpr int tile_floats() { return kTile * (D + 2); }
+
+// sum over i < n of floor((a i + b) / m)
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  long long ans = 0;
+  while (n > 0) {
+    if (a >= m) {
+      ans += (long long)n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += (long long)n * (b / m);
+      b %= m;
+    }
+    const uint32_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return ans;
+}
+
+// What a step-line needs to know of one sequence.
+struct PromptSeq {
+  int q0, n, k0, len, past, pairs;  // past = len - n: keys before the first query (negative: fewer keys)
+};
+
+struct PromptCost {
+  const int *cu_q, *cu_k;
+  int Tq, Tk, TQ, H_kv, causal;
+  __device__ PromptSeq seq(int b) const {
+    const SeqRows q = seq_rows(cu_q, b, Tq), k = seq_rows(cu_k, b, Tk);
+    return {q.begin, q.n, k.begin, k.n, k.n - q.n, (q.n + 2 * TQ - 1) / (2 * TQ)};
+  }
+  // keys that the queries below token index t of the sequence see at most
+  __device__ int limit(const PromptSeq &s, int t) const { return causal ? s.past + min(t, s.n) : s.len; }
+  __device__ int steps(const PromptSeq &s, int pair) const {
+    return max(1, (limit(s, (pair + 1) * 2 * TQ) + kTile - 1) >> 7);
+  }
+  // steps of the pairs before `pair` (< s.pairs), all of them full
+  __device__ long long before(const PromptSeq &s, int pair) const {
+    if (!causal) return (long long)pair * max(1, (s.len + kTile - 1) >> 7);
+    const int R = 2 * TQ;
+    const int ones = min(pair, s.past >= kTile ? 0 : (kTile - s.past) / R);  // pairs of one step
+    return ones + floor_sum(pair - ones, kTile, R, (uint32_t)(s.past + (ones + 1) * R + kTile - 1));
+  }
+  __device__ long long head(const PromptSeq &s) const {
+    return s.pairs ? before(s, s.pairs - 1) + steps(s, s.pairs - 1) : 0;
+  }
+  __device__ long long cost(int b) const { return head(seq(b)) * H_kv; }
+  // whole warp: 32-way search for the last pair that starts at or before off; tag = the pair's number h * pairs + pair
+  __device__ int item(int b, long long off, long long *s, long long *e) const {
+    const PromptSeq q = seq(b);
+    const long long line = head(q);
+    const int h = (int)(off / line);
+    const long long rem = off - h * line;
+    int lo = 0, n = q.pairs;
+    const int lane = threadIdx.x & 31;
+    while (n > 1) {
+      const int step = (n + 31) >> 5;
+      const int at = min(lane * step, n - 1);
+      const unsigned le = __ballot_sync(0xffffffffu, before(q, lo + at) <= rem);
+      const int k = (__popc(le) - 1) * step;  // lane 0 always is
+      const int skip = min(k, n - 1);
+      lo += skip;
+      n = min(step, n - skip);
+    }
+    *s = h * line + before(q, lo);
+    *e = *s + steps(q, lo);
+    return h * q.pairs + lo;
+  }
+};
+
+// One item, or the part of it that falls in this CTA's stretch.
+struct PromptSeg {
+  PromptSeq s;
+  int b, h, pair;
+  int j0, j1, total;     // KV tiles [j0, j1) of total
+  __device__ bool whole() const { return j0 == 0 && j1 == total; }
+};
+
+// Every role walks the same segments.
+struct PromptWalk {
+  long long left;
+  int b, h, pair, j;
+  PromptSeq s;
+  __device__ void start(const PromptCost &c, const SplitRange &r) {
+    left = r.x1 - r.x0;
+    b = r.b;
+    if (left <= 0) return;
+    s = c.seq(b);
+    h = s.pairs ? r.tag / s.pairs : 0;
+    pair = s.pairs ? r.tag % s.pairs : 0;
+    j = (int)(r.off - r.begin);
+  }
+  __device__ bool next(const PromptCost &c, int B, PromptSeg &g) {
+    if (left <= 0) return false;
+    int total = pair < s.pairs ? c.steps(s, pair) : 0;
+    while (j >= total) {  // on to the next item that has steps
+      j = 0;
+      if (++pair >= s.pairs) {
+        pair = 0;
+        if (++h >= c.H_kv || s.pairs == 0) {
+          h = 0;
+          do {
+            if (++b >= B) return false;
+            s = c.seq(b);
+          } while (s.pairs == 0);
+        }
+      }
+      total = c.steps(s, pair);
+    }
+    g.s = s;
+    g.b = b;
+    g.h = h;
+    g.pair = pair;
+    g.j0 = j;
+    g.total = total;
+    g.j1 = (int)min((long long)total, j + left);
+    left -= g.j1 - g.j0;
+    j = g.j1;
+    return true;
+  }
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE = HALVES * kBox;
+  static constexpr int STAGES = D == 128 ? 5 : 8;
+};
+
+template <int D>
+struct PromptSmem {
+  uint8_t q[2][Cfg<D>::TILE];
+  uint8_t ring[Cfg<D>::STAGES][Cfg<D>::TILE];
+  uint64_t full[Cfg<D>::STAGES], empty[Cfg<D>::STAGES];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t drain;
+  long long scratch[kThreads / 32 + 6];
+  SplitRange range;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) { return pack_half2(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int y, int z, int w,
+                                            int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      : "memory");
+}
+
+// Last KV tile (exclusive) of the pair's tile w inside the segment: [j0, end).
+__device__ __forceinline__ int seg_end(const PromptCost &c, const PromptSeg &g, int w) {
+  if (w == 1 && (g.pair * 2 + 1) * c.TQ >= g.s.n) return g.j0;  // no rows in tile B
+  const int lim = c.limit(g.s, (g.pair * 2 + w + 1) * c.TQ);
+  return max(g.j0, min(g.j1, lim > 0 ? (lim + kTile - 1) >> 7 : 0));
+}
+
+template <int D, typename T, typename TO>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, PromptParams P) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  PromptSmem<D> &sm =
+      *reinterpret_cast<PromptSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int *abort = &sm.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PromptCost cost = {P.cu_q, P.cu_k, P.Tq, P.Tk, P.TQ, P.H_kv, P.causal};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sm.s_full[w], 1);
+      mbar_init(&sm.p_full[w], 128);
+      mbar_init(&sm.o_final[w], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+    P.meta[2 * blockIdx.x].state = 0;
+    P.meta[2 * blockIdx.x + 1].state = 0;
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kMinPart, &sm.range, sm.scratch);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  PromptWalk walk;
+  walk.start(cost, sm.range);
+  PromptSeg g;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        uint32_t n_ring = 0, pend = 0, ph_bits = 0, n_q = 0;
+        bool ok = true;
+        auto load = [&](const CUtensorMap *m, int row, int h) {
+          const uint32_t st = n_ring % C::STAGES, ph = (n_ring / C::STAGES) & 1;
+          ++n_ring;
+          if (!wait_parity(&sm.empty[st], ph ^ 1, P.err, abort, 51)) return false;
+          mbar_arrive_expect_tx(&sm.full[st], C::TILE);
+          tma_load_4d(sm.ring[st], m, &sm.full[st], 0, row, 0, h);
+          pend |= 1u << st;
+          ph_bits = (ph_bits & ~(1u << st)) | (ph << st);
+          return true;
+        };
+        while (ok && walk.next(cost, P.B, g)) {
+          if (g.j0 == 0 && (seq_rows_bad(P.cu_q, g.b, P.Tq) || seq_rows_bad(P.cu_k, g.b, P.Tk)))
+            report_error(P.err, ISPA_ERR_INVALID_ARG, g.b);
+          const int end0 = seg_end(cost, g, 0), end1 = seg_end(cost, g, 1), end = max(end0, end1);
+          if (end == g.j0) continue;  // no key in sight: nothing to load
+          ok = wait_parity(&sm.q_empty, (n_q & 1) ^ 1, P.err, abort, 52);
+          if (!ok) break;
+          const int rows = P.G * P.TQ;
+          mbar_arrive_expect_tx(&sm.q_full, 2 * C::HALVES * rows * 128);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int f = 0; f < C::HALVES; ++f)
+              tma_load_5d(sm.q[w] + f * kBox, &tq, &sm.q_full, 0, 0, g.s.q0 + (g.pair * 2 + w) * P.TQ, f, g.h);
+          ++n_q;
+          for (int j = g.j0; ok && j < end; ++j) {
+            ok = load(&tk, g.s.k0 + j * kTile, g.h);
+            if (ok) ok = load(&tv, g.s.k0 + j * kTile, g.h);
+          }
+        }
+        if (*abort) {  // let copies in flight land before the CTA exits
+          for (int st = 0; st < C::STAGES; ++st)
+            if (pend & (1u << st)) wait_parity_drain(&sm.full[st], (ph_bits >> st) & 1, P.err);
+          if (n_q) wait_parity_drain(&sm.q_full, (n_q - 1) & 1, P.err);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr int fmt = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0 : 1;
+      constexpr uint32_t idesc_s = make_idesc(128, 128, fmt, 0, 0);   // Q (K-major) x K (K-major)
+      constexpr uint32_t idesc_pv = make_idesc(128, D, fmt, 0, 1);    // P (TMEM) x V (MN-major)
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+      const uint64_t dring_k = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
+      const uint64_t dring_v = smem_desc_sw128(smem_u32(sm.ring[0]), kBox, 1024);
+      uint32_t n_ring = 0, n_q = 0, n_p[2] = {0, 0};
+      bool ok = true;
+      auto ring_wait = [&](uint32_t k, int site) {
+        return wait_parity(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, P.err, abort, site);
+      };
+      auto issue_s = [&](int w, uint32_t k) {
+        const uint64_t qd = dq0 + (uint64_t)((w * C::TILE) >> 4);
+        const uint64_t kd = dring_k + (uint64_t)(((k % C::STAGES) * C::TILE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
+          mma_ss(tmem + kColS + w * 128, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u, 0);
+        }
+        mma_commit(&sm.s_full[w]);
+      };
+      while (ok && walk.next(cost, P.B, g)) {
+        const int end0 = seg_end(cost, g, 0), end1 = seg_end(cost, g, 1), end = max(end0, end1);
+        if (end == g.j0) continue;
+        ok = wait_parity(&sm.q_full, n_q & 1, P.err, abort, 53) && ring_wait(n_ring, 54);
+        ++n_q;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t kn = n_ring;  // ring number of the K tile whose S was issued last
+        if (lane == 0) {
+          if (g.j0 < end0) issue_s(0, kn);
+          if (g.j0 < end1) issue_s(1, kn);
+          mma_commit(&sm.empty[kn % C::STAGES]);
+          if (end == g.j0 + 1) mma_commit(&sm.q_empty);
+        }
+        for (int j = g.j0; j < end; ++j) {
+          const uint32_t vn = n_ring + 1;
+          kn = n_ring + 2;
+          n_ring += 2;
+          ok = ring_wait(vn, 55);
+          if (ok && j + 1 < end) ok = ring_wait(kn, 56);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int left = g.s.len - j * kTile;  // keys of the sequence in this tile
+          if (left < kTile && (left & 15)) {
+            // rows left .. the end of their 16-key step belong to the next sequence
+            uint8_t *v = sm.ring[vn % C::STAGES];
+            const int n16 = (16 - (left & 15)) * 8;
+            for (int i = lane; i < n16 * C::HALVES; i += 32)
+              *reinterpret_cast<uint4 *>(v + (i / n16) * kBox + left * 128 + (i % n16) * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int my_end = w ? end1 : end0;
+            if (j >= my_end) continue;
+            ok = wait_parity_spin(&sm.p_full[w], n_p[w] & 1, P.err, abort, 57 + w);
+            ++n_p[w];
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const int seen = min(kTile, cost.limit(g.s, (g.pair * 2 + w + 1) * P.TQ) - j * kTile);
+              const int k_steps = (seen + 15) >> 4;
+              const uint64_t vd = dring_v + (uint64_t)(((vn % C::STAGES) * C::TILE) >> 4);
+              const uint32_t a_p = tmem + kColS + w * 128, d_o = tmem + kColO + w * 128;
+              if (k_steps == 8) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > g.j0 || kk > 0) ? 1u : 0u);
+              } else {
+                for (int kk = 0; kk < k_steps; ++kk)
+                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > g.j0 || kk > 0) ? 1u : 0u);
+              }
+              if (j + 1 < my_end)
+                issue_s(w, kn);
+              else
+                mma_commit(&sm.o_final[w]);
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mma_commit(&sm.empty[vn % C::STAGES]);
+            if (j + 1 < end) mma_commit(&sm.empty[kn % C::STAGES]);
+            if (j + 2 == end) mma_commit(&sm.q_empty);
+          }
+        }
+      }
+      if (!ok && lane == 0) {
+        mma_commit(&sm.drain);
+        wait_parity_drain(&sm.drain, 0, P.err);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int w = (warp >> 2) - 1;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
+    const int tok = r / P.G, head = r % P.G;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t col_s = lane_base + kColS + w * 128, col_o = lane_base + kColO + w * 128;
+    uint32_t n_s = 0, n_o = 0;
+    bool ok = true;
+    while (ok && walk.next(cost, P.B, g)) {
+      const int qi = (g.pair * 2 + w) * P.TQ + tok;  // this row's token in its sequence
+      const bool row_ok = tok < P.TQ && qi < g.s.n;
+      const int lim = P.causal ? g.s.past + qi + 1 : g.s.len;
+      const int lim_first = P.causal ? g.s.past + (g.pair * 2 + w) * P.TQ + 1 : g.s.len;
+      const int end = seg_end(cost, g, w);
+      float m_ref = 0.f, l = 0.f;
+      for (int j = g.j0; j < end; ++j) {
+        ok = wait_parity_spin(&sm.s_full[w], n_s & 1, P.err, abort, 61 + w);
+        ++n_s;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(col_s + c * 32, sr[c]);
+        tmem_wait_ld();
+        if ((j + 1) * kTile > lim_first) {  // the diagonal, or the sequence's end
+          const int valid = lim - j * kTile;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= valid) sr[c >> 5][c & 31] = 0xff800000u;
+        }
+        float mx[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mx[t] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 2)
+          mx[(c >> 1) & 7] = max3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
+                                  __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
+        const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * P.scale_log2;
+        if (j == g.j0) {
+          m_ref = mt == -INFINITY ? 0.f : mt;
+        } else if (__any_sync(0xffffffffu, mt > m_ref + kThreshold)) {
+          const float m_new = fmaxf(m_ref, mt);
+          const float f = exp2_fast(m_ref - m_new);
+          m_ref = m_new;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(col_o + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
+            tmem_st16(col_o + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+            tmem_st16(col_o + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+          }
+        }
+        // P = 2^(s scale log2e - m_ref) <= 2^8 in the input type, over the first 64 columns of S
+        const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            const float2 x =
+                fma2(make_float2(__uint_as_float(sr[c][2 * t]), __uint_as_float(sr[c][2 * t + 1])), sc2, nm2);
+            const float2 pp = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            ls[t & 1] = add2(ls[t & 1], pp);
+            pk[t] = pack2<T>(pp.x, pp.y);
+          }
+          tmem_st16(col_s + c * 16, pk);
+        }
+        tmem_wait_st();
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[w]);
+      }
+      if (!ok) break;
+      // ---- the segment's output
+      if (end > g.j0) {
+        ok = wait_parity(&sm.o_final[w], n_o & 1, P.err, abort, 63 + w);
+        ++n_o;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool some = l > 0.f;
+      if (g.whole()) {
+        const long long out = ((long long)(g.s.q0 + (row_ok ? qi : 0)) * P.H + g.h * P.G + head);
+        const float inv = some ? 1.f / l : 0.f;
+        TO *dst = static_cast<TO *>(P.o) + out * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t raw[32];
+          if (end > g.j0) {
+            tmem_ld32(col_o + c * 32, raw);
+            tmem_wait_ld();
+          }
+          if (!row_ok) continue;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            float x[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) x[t] = some ? __uint_as_float(raw[8 * v + t]) * inv : 0.f;
+            store8(dst + c * 32 + v * 8, x);
+          }
+        }
+        if (row_ok && P.lse) P.lse[out] = some ? (m_ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      } else {
+        const int slot = 2 * blockIdx.x + (g.j0 == 0 ? 1 : 0);
+        float *part = P.part + ((size_t)slot * 2 + w) * tile_floats<D>();
+        part[r] = some ? m_ref : -INFINITY;
+        part[kTile + r] = l;
+        float4 *po = reinterpret_cast<float4 *>(part + 2 * kTile);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t raw[32];
+          if (end > g.j0) {
+            tmem_ld32(col_o + c * 32, raw);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            po[(c * 8 + v) * kTile + r] =
+                some ? make_float4(__uint_as_float(raw[4 * v]), __uint_as_float(raw[4 * v + 1]),
+                                   __uint_as_float(raw[4 * v + 2]), __uint_as_float(raw[4 * v + 3]))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (w == 0 && r == 0) {
+          PartMeta *m = P.meta + slot;
+          m->b = g.b;
+          m->item = g.h * g.s.pairs + g.pair;
+          m->state = g.j1 == g.total ? 2 : 1;
+        }
+      }
+      tc_fence_before();  // O is read before the p_full that lets the next item overwrite it
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the item that slot 2c + 1 starts: block (c, tile, 32 columns), one row per thread.
+template <int D, typename TO>
+__global__ void __launch_bounds__(kTile) prompt_merge_kernel(PromptParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, w = blockIdx.y, c0 = blockIdx.z * 32, r = threadIdx.x;
+  const int n = part_count(P.meta, P.nc, c);
+  if (n == 0) return;
+  const PromptCost cost = {P.cu_q, P.cu_k, P.Tq, P.Tk, P.TQ, P.H_kv, P.causal};
+  const int b = P.meta[2 * c + 1].b, item = P.meta[2 * c + 1].item;
+  const PromptSeq s = cost.seq(b);
+  const int h = item / s.pairs, pair = item % s.pairs;
+  const int tok = r / P.G, head = r % P.G, qi = (pair * 2 + w) * P.TQ + tok;
+  if (tok >= P.TQ || qi >= s.n) return;
+  auto at = [&](int k) { return P.part + ((size_t)part_slot(c, k) * 2 + w) * tile_floats<D>(); };
+  float mm = -INFINITY;
+  for (int k = 0; k < n; ++k) mm = fmaxf(mm, at(k)[r]);
+  const float ref = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f, x[32] = {};
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    const float *p = at(k);
+    const float f = exp2_fast(p[r] - ref);
+    ll += p[kTile + r] * f;
+    const float4 *po = reinterpret_cast<const float4 *>(p + 2 * kTile) + (c0 / 4) * kTile + r;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const float4 a = po[v * kTile];
+      x[4 * v] += a.x * f, x[4 * v + 1] += a.y * f, x[4 * v + 2] += a.z * f, x[4 * v + 3] += a.w * f;
+    }
+  }
+  const long long out = (long long)(s.q0 + qi) * P.H + h * P.G + head;
+  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    float y[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) y[t] = x[8 * v + t] * inv;
+    store8(static_cast<TO *>(P.o) + out * D + c0 + v * 8, y);
+  }
+  if (P.lse && c0 == 0) P.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+}
+
+template <int D, typename T, typename TO>
+ispa_status launch_one(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PromptParams &P,
+                       cudaStream_t s) {
+  auto kern = attn_prompt_kernel<D, T, TO>;
+  constexpr int smem = sizeof(PromptSmem<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_status(e, "attn_prompt shared memory");
+  kern<<<P.nc, kThreads, smem, s>>>(tq, tk, tv, P);
+  note_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e, "attn_prompt launch");
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.nc, 2, D / 32);
+  cfg.blockDim = dim3(kTile);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prompt_merge_kernel<D, TO>, P);
+  note_launch();
+  return cuda_status(e, "prompt_merge launch");
+}
+
+template <int D>
+ispa_status launch_typed(const ispa_attn_seq_desc &d, const CUtensorMap &tq, const CUtensorMap &tk,
+                         const CUtensorMap &tv, const PromptParams &P, cudaStream_t s) {
+  const bool f32 = d.out_dtype == ISPA_F32;
+  if (d.in_dtype == ISPA_BF16)
+    return f32 ? launch_one<D, __nv_bfloat16, float>(tq, tk, tv, P, s)
+               : launch_one<D, __nv_bfloat16, __nv_bfloat16>(tq, tk, tv, P, s);
+  return f32 ? launch_one<D, __half, float>(tq, tk, tv, P, s) : launch_one<D, __half, __half>(tq, tk, tv, P, s);
+}
+
+}  // namespace
+
+size_t attn_prompt_workspace_bytes(int head_dim) {
+  const size_t nc = sm_count();
+  return 2 * nc * (sizeof(PartMeta) + (size_t)2 * kTile * (head_dim + 2) * 4);
+}
+
+ispa_status launch_attn_prompt(const ispa_attn_seq_desc &d, float scale, int Tq, int Tk, const int *cu_q,
+                               const int *cu_k, const void *q, long long qs, const void *k, long long ks,
+                               const void *v, long long vs, void *o, float *lse, void *workspace, cudaStream_t s) {
+  PromptParams P;
+  ispa_status st = device_err(&P.err);
+  if (st != ISPA_OK) return st;
+  P.B = d.B;
+  P.H = d.H;
+  P.H_kv = d.H_kv;
+  P.G = d.H / d.H_kv;
+  P.TQ = kTile / P.G;
+  P.Tq = Tq;
+  P.Tk = Tk;
+  P.causal = d.causal;
+  P.nc = sm_count();
+  P.scale_log2 = scale * 1.4426950408889634f;
+  P.cu_q = cu_q;
+  P.cu_k = cu_k;
+  P.o = o;
+  P.lse = lse;
+  P.meta = static_cast<PartMeta *>(workspace);
+  P.part = reinterpret_cast<float *>(P.meta + 2 * P.nc);
+  const CUtensorMapDataType dt =
+      d.in_dtype == ISPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int D = d.head_dim;
+  CUtensorMap tq, tk, tv;
+  {
+    // 64 columns | heads of the group | tokens | column halves | K/V heads
+    const uint64_t dims[5] = {64, (uint64_t)P.G, (uint64_t)Tq, (uint64_t)D / 64, (uint64_t)d.H_kv};
+    const uint64_t str[4] = {(uint64_t)D * 2, (uint64_t)qs * 2, 128, (uint64_t)P.G * D * 2};
+    const uint32_t box[5] = {64, (uint32_t)P.G, (uint32_t)P.TQ, 1, 1};
+    st = make_tmap(&tq, dt, 5, q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != ISPA_OK) return st;
+  }
+  for (int i = 0; i < 2; ++i) {
+    // without a key (Tk == 0) no tile is loaded: the maps then describe q's first rows
+    const uint64_t dims[4] = {64, (uint64_t)std::max(Tk, 1), (uint64_t)D / 64, (uint64_t)d.H_kv};
+    const uint64_t str[3] = {(uint64_t)(i ? vs : ks) * 2, 128, (uint64_t)D * 2};
+    const uint32_t box[4] = {64, (uint32_t)kTile, (uint32_t)D / 64, 1};
+    st = make_tmap(i ? &tv : &tk, dt, 4, Tk == 0 ? q : (i ? v : k), dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != ISPA_OK) return st;
+  }
+  return D == 128 ? launch_typed<128>(d, tq, tk, tv, P, s) : launch_typed<64>(d, tq, tk, tv, P, s);
+}
+
+}  // namespace ispa

@@ -118,4 +118,20 @@ ispa_status launch_quant_cols(int K, int N, const void *W, int fmt, void *qT, fl
 ispa_status launch_gemm_q8(int M, int N, int K, const void *qa, const float *sa, const void *qT, const float *sw,
                            int fmt, void *y, ispa_dtype ydt, cudaStream_t s);
 
+// sequences: the quantised paged cache (kvq.cu), attention over it (attn_kvq.cu)
+// and over packed prompts (attn_prompt.cu)
+ispa_status launch_kvq_write(const ispa_kvq_desc &d, int B, int T, const int *table, int max_pages, const int *lens,
+                             const int *cu, const void *k, long long ks, const void *v, long long vs, ispa_dtype dt,
+                             void *kvq, cudaStream_t s);
+ispa_status launch_kvq_read(const ispa_kvq_desc &d, int B, int T, const int *table, int max_pages, const int *begin,
+                            const int *cu, const void *kvq, void *ko, void *vo, ispa_dtype dt, cudaStream_t s);
+size_t attn_kvq_workspace_bytes(int head_dim);
+ispa_status launch_attn_kvq(const ispa_attn_seq_desc &d, const ispa_kvq_desc &c, float scale, int T, const int *cu_q,
+                            const int *table, int max_pages, const int *lens, const void *q, long long qs,
+                            const void *kvq, void *o, float *lse, void *workspace, cudaStream_t s);
+size_t attn_prompt_workspace_bytes(int head_dim);
+ispa_status launch_attn_prompt(const ispa_attn_seq_desc &d, float scale, int Tq, int Tk, const int *cu_q,
+                               const int *cu_k, const void *q, long long qs, const void *k, long long ks,
+                               const void *v, long long vs, void *o, float *lse, void *workspace, cudaStream_t s);
+
 }  // namespace ispa

@@ -1,0 +1,193 @@
+// seq.cuh -- packed sequences: bounds read from device arrays, and the even
+// split of ragged work over a fixed number of CTAs that the two sequence
+// attentions share.
+//
+// The work of one call is a line of unit steps: sequences in order, each
+// sequence's items (a query tile of a head) in order, each item's KV tiles in
+// order.  CTA c of n takes the stretch [c * total / n, (c + 1) * total / n), so
+// every SM gets the same number of steps whatever the lengths are.  An item
+// that a boundary cuts is finished from partial results: each CTA leaves at
+// most two (the end of an item that began before its stretch, slot 2c, and the
+// start of one that goes on behind it, slot 2c + 1), and a second launch
+// merges them.  A boundary that would cut off a part of fewer than min_part
+// steps moves to the item's edge.
+#pragma once
+
+#include "common.cuh"
+
+namespace ispa {
+
+// Rows [begin, begin + n) of sequence b, clamped to the T rows that exist.
+struct SeqRows {
+  int begin, n;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const int *cu, int b, int T) {
+  const int c0 = min(max(__ldg(cu + b), 0), T), c1 = min(max(__ldg(cu + b + 1), 0), T);
+  return {c0, max(0, c1 - c0)};
+}
+
+__device__ __forceinline__ bool seq_rows_bad(const int *cu, int b, int T) {
+  const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+  return c0 < 0 || c1 < c0 || c1 > T;
+}
+
+__device__ __forceinline__ int seq_len(const int *lens, int b, int cap) {
+  return min(max(__ldg(lens + b), 0), cap);
+}
+
+// The sequence that owns packed row t, or -1; executed by a whole warp with a
+// uniform t.  Each round narrows the candidates 32-fold by a ballot, so that
+// 1024 sequences cost two dependent loads.
+__device__ __forceinline__ int seq_of_row(const int *cu, int B, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // the first b in [lo, lo + n) with cu[b + 1] > t
+  while (n > 0) {
+    const int step = (n + 31) >> 5;
+    const int b = lo + min((lane + 1) * step, n) - 1;  // last candidate of this lane's part
+    const unsigned past = __ballot_sync(0xffffffffu, __ldg(cu + b + 1) <= t);
+    const int k = __popc(past);  // parts that end at or before t
+    if (k == 32) return -1;
+    const int skip = min(k * step, n);
+    lo += skip;
+    n = min(step, n - skip);
+    if (step == 1) break;
+  }
+  return n > 0 && lo < B && __ldg(cu + lo) <= t ? lo : -1;
+}
+
+struct SplitRange {
+  int b;             // sequence that holds the first step
+  int tag;           // f.item()'s name of the item
+  long long off;     // the step's place in the sequence's line
+  long long begin;   // and the item's
+  long long x0, x1;  // the stretch [x0, x1) of the whole line
+};
+
+// This CTA's stretch.  f.cost(b): steps of sequence b; f.item(b, off, &s, &e)
+// (called by a whole warp): the item [s, e) that holds step off of sequence b.
+// At most ceil(total / min_unit) CTAs get work.  Called by all NT threads; sw:
+// NT / 32 + 6 values of scratch.
+template <int NT, class F>
+__device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int min_part, SplitRange *r,
+                            long long *sw) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (B + NT - 1) / NT;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += f.cost(b);
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) sw[warp] = inc;
+  long long *found = sw + NT / 32;  // per boundary: sequence (-1: none), place in it, place of the sequence
+  if (tid < 2) found[3 * tid] = -1;
+  __syncthreads();
+  long long pre = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) pre += sw[w];
+    total += sw[w];
+  }
+  const long long want = (total + min_unit - 1) / min_unit;
+  const int n = (int)(want < nc ? (want > 0 ? want : 1) : nc);
+  if (tid == 0) {
+    r->b = 0;
+    r->tag = 0;
+    r->off = 0;
+    r->begin = 0;
+    r->x0 = c < n ? 0 : total;
+    r->x1 = total;
+  }
+  if (c < n) {
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const long long x = (long long)(c + k) * total / n;
+      if (x <= 0 || x >= total || x < pre || x >= pre + mine) continue;
+      long long p = pre;
+      for (int b = b0; b < b1; ++b) {
+        const long long cb = f.cost(b);
+        if (x < p + cb) {
+          found[3 * k] = b;
+          found[3 * k + 1] = x - p;
+          found[3 * k + 2] = p;
+          break;
+        }
+        p += cb;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp < 2 && found[3 * warp] >= 0) {
+    const int b = (int)found[3 * warp];
+    long long off = found[3 * warp + 1], s, e;
+    const int tag = f.item(b, off, &s, &e);
+    if (off - s < min_part) off = s;
+    else if (e - off < min_part) off = e;
+    if (lane == 0) {
+      if (warp == 0) {
+        r->b = b;
+        r->tag = tag;
+        r->off = off;
+        r->begin = s;
+        r->x0 = found[2] + off;
+      } else {
+        r->x1 = found[5] + off;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// What a CTA records of its two partial results (slots 2c and 2c + 1).
+struct PartMeta {
+  int state;  // 0: none, 1: the item goes on in the next CTA, 2: the item ends here
+  int b, item, spare;
+};
+
+// A stretch's first CTA owns an item that slot 2c + 1 starts; its parts are
+// that slot and slots 2c' of the CTAs behind it up to the first with state 2.
+// Returns their number (0: nothing to merge); part i > 0 is in slot 2 (c + i).
+__device__ __forceinline__ int part_count(const volatile PartMeta *meta, int nc, int c) {
+  if (meta[2 * c + 1].state == 0) return 0;
+  int n = 1;
+  while (c + n < nc) {
+    const int st = meta[2 * (c + n)].state;
+    if (st == 0) break;
+    ++n;
+    if (st == 2) break;
+  }
+  return n;
+}
+
+__device__ __forceinline__ int part_slot(int c, int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); }
+
+// 16-byte stores of eight fp32 values in the output's type.
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void store8(__half *p, const float (&x)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]),
+                                             pack_half2(x[6], x[7]));
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t w, const __half *) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, const __nv_bfloat16 *) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+}
+
+}  // namespace ispa
