@@ -232,6 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
   const int g = lane >> 2, t4 = lane & 3;
   const KvqCost cost = {P.cu, P.lens, P.T, P.cap, P.G, P.c.H_kv};
   if (threadIdx.x < 2) P.meta[2 * blockIdx.x + threadIdx.x].state = 0;
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < P.B; b += kThreads)
+      if (seq_rows_bad(P.cu, b, P.T) || __ldg(P.lens + b) != seq_len(P.lens, b, P.cap)) report_seq(P.err, b);
   split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, kMinUnit, kMinPart, &range, scratch);
 
   long long left = range.x1 - range.x0;
@@ -254,10 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
     const int t_end = (int)min((long long)tiles, t_begin + left);
     const int h = item / blocks, rb = item % blocks;
     const int n_rows = min(kRows, rows.n * P.G - rb * kRows);
-    if (threadIdx.x == 0 && t_begin == 0 && (seq_rows_bad(P.cu, b, P.T) || __ldg(P.lens + b) != len)) {
-      if (atomicCAS(P.err, 0, ISPA_ERR_INVALID_ARG) == 0) atomicExch(P.err + 1, b);
-    }
-
     // ---- this warp's first tiles are on their way while Q is laid out
     const int my0 = t_begin + warp;
     int bad = 0;
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
         }
       }
     }
-    if (bad && lane == 0 && atomicCAS(P.err, 0, ISPA_ERR_INVALID_ARG) == 0) atomicExch(P.err + 1, b);
+    if (bad && lane == 0) report_seq(P.err, b);
 
     // ---- merge the warps' states (the rings are idle now)
     cp_wait<0>();

@@ -11,7 +11,10 @@
 //   0      TMA producer: the pair's Q tiles, then K_0, V_0, K_1, V_1, ... through
 //          one ring of stages
 //   1      TMEM allocator and MMA issuer (whole warp; one lane issues)
-//   2, 3   idle
+//   2      scheduler: walks the stretch and hands the items on through a ring in shared memory, so that
+//          no role on the critical path holds the walk's state (when every role walked for itself, the
+//          spilled registers went to L2 -- shared memory leaves no L1 -- and a step took 14 k cycles)
+//   3      idle
 //   4-7    softmax and output of tile A, one row per thread (TMEM lane = row)
 //   8-11   the same for tile B
 // TMEM: S of A [0,128), S of B [128,256), O of A [256,256+d), O of B [384,384+d).
@@ -50,6 +53,8 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr int kBox = 128 * 128;  // bytes of 128 rows x 64 columns
 constexpr int kMinPart = 4;
+constexpr int kSegs = 4;         // items handed on ahead
+constexpr int kSegReaders = 10;  // producer, issuer, eight softmax warps
 constexpr float kThreshold = 8.0f;  // the reference maximum moves when passed by more than this (log2)
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -142,15 +147,16 @@ struct PromptCost {
   }
 };
 
-// One item, or the part of it that falls in this CTA's stretch.
+// One item, or the part of it that falls in this CTA's stretch, as the roles see it.
 struct PromptSeg {
-  PromptSeq s;
-  int b, h, pair;
-  int j0, j1, total;     // KV tiles [j0, j1) of total
-  __device__ bool whole() const { return j0 == 0 && j1 == total; }
+  int mode;             // -1: no more work, 0: a part (result to `slot`), 1: the whole item
+  int slot, h;
+  int q_row, n_tok;     // first row of the pair's tokens, tokens of the pair (up to 2 TQ)
+  int k_row, len, lim;  // first key row, keys, keys that the pair's first token sees
+  int j0, end[2];       // KV tiles [j0, end[w]) of tile w
 };
 
-// Every role walks the same segments.
+// The scheduler's walk over the stretch.
 struct PromptWalk {
   long long left;
   int b, h, pair, j;
@@ -164,7 +170,7 @@ struct PromptWalk {
     pair = s.pairs ? r.tag % s.pairs : 0;
     j = (int)(r.off - r.begin);
   }
-  __device__ bool next(const PromptCost &c, int B, PromptSeg &g) {
+  __device__ bool next(const PromptCost &c, int B, PromptSeg &g, PartMeta *meta) {
     if (left <= 0) return false;
     int total = pair < s.pairs ? c.steps(s, pair) : 0;
     while (j >= total) {  // on to the next item that has steps
@@ -181,15 +187,29 @@ struct PromptWalk {
       }
       total = c.steps(s, pair);
     }
-    g.s = s;
-    g.b = b;
+    const int j1 = (int)min((long long)total, j + left);
+    const int t0 = pair * 2 * c.TQ;
     g.h = h;
-    g.pair = pair;
+    g.q_row = s.q0 + t0;
+    g.n_tok = min(2 * c.TQ, s.n - t0);
+    g.k_row = s.k0;
+    g.len = s.len;
+    g.lim = c.causal ? s.past + t0 + 1 : s.len;
     g.j0 = j;
-    g.total = total;
-    g.j1 = (int)min((long long)total, j + left);
-    left -= g.j1 - g.j0;
-    j = g.j1;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int lim = g.n_tok > w * c.TQ ? c.limit(s, t0 + (w + 1) * c.TQ) : 0;
+      g.end[w] = max(j, min(j1, (lim + kTile - 1) >> 7));
+    }
+    g.slot = j == 0 ? 1 : 0;
+    g.mode = j == 0 && j1 == total ? 1 : 0;
+    if (g.mode == 0) {
+      meta[g.slot].b = b;
+      meta[g.slot].item = h * s.pairs + pair;
+      meta[g.slot].state = j1 == total ? 2 : 1;
+    }
+    left -= j1 - j;
+    j = j1;
     return true;
   }
 };
@@ -209,6 +229,8 @@ struct PromptSmem {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_final[2];
   uint64_t drain;
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  PromptSeg seg[kSegs];
   long long scratch[kThreads / 32 + 6];
   SplitRange range;
   uint32_t tmem_base;
@@ -260,13 +282,6 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *m, uin
       : "memory");
 }
 
-// Last KV tile (exclusive) of the pair's tile w inside the segment: [j0, end).
-__device__ __forceinline__ int seg_end(const PromptCost &c, const PromptSeg &g, int w) {
-  if (w == 1 && (g.pair * 2 + 1) * c.TQ >= g.s.n) return g.j0;  // no rows in tile B
-  const int lim = c.limit(g.s, (g.pair * 2 + w + 1) * c.TQ);
-  return max(g.j0, min(g.j1, lim > 0 ? (lim + kTile - 1) >> 7 : 0));
-}
-
 template <int D, typename T, typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -292,6 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.o_final[w], 1);
     }
     mbar_init(&sm.drain, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&sm.seg_full[i], 1);
+      mbar_init(&sm.seg_empty[i], kSegReaders);
+    }
     sm.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tq);
@@ -300,19 +319,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     P.meta[2 * blockIdx.x].state = 0;
     P.meta[2 * blockIdx.x + 1].state = 0;
   }
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < P.B; b += kThreads)
+      if (seq_rows_bad(P.cu_q, b, P.Tq) || seq_rows_bad(P.cu_k, b, P.Tk)) report_error(P.err, ISPA_ERR_INVALID_ARG, b);
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
   split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kMinPart, &sm.range, sm.scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  PromptWalk walk;
-  walk.start(cost, sm.range);
-  PromptSeg g;
+  // item i of the stretch, for the roles: seg_wait, read, seg_done
+  uint32_t n_seg = 0;
+  auto seg_wait = [&]() -> const PromptSeg * {
+    const uint32_t i = n_seg % kSegs;
+    return wait_parity(&sm.seg_full[i], (n_seg / kSegs) & 1, P.err, abort, 50) ? &sm.seg[i] : nullptr;
+  };
+  auto seg_done = [&]() {  // one lane of each reading warp
+    mbar_arrive(&sm.seg_empty[n_seg % kSegs]);
+    ++n_seg;
+  };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
+    if (warp == 2) {
+      // ---------------------------------------------------------- scheduler
+      if (lane == 0) {
+        PromptWalk walk;
+        walk.start(cost, sm.range);
+        for (bool more = true; more; ++n_seg) {
+          const uint32_t i = n_seg % kSegs;
+          if (!wait_parity(&sm.seg_empty[i], ((n_seg / kSegs) & 1) ^ 1, P.err, abort, 49)) break;
+          PromptSeg g;
+          more = walk.next(cost, P.B, g, P.meta + 2 * blockIdx.x);
+          if (!more) g.mode = -1;
+          sm.seg[i] = g;
+          mbar_arrive(&sm.seg_full[i]);
+        }
+      }
+    } else if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
         uint32_t n_ring = 0, pend = 0, ph_bits = 0, n_q = 0;
@@ -327,24 +370,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph_bits = (ph_bits & ~(1u << st)) | (ph << st);
           return true;
         };
-        while (ok && walk.next(cost, P.B, g)) {
-          if (g.j0 == 0 && (seq_rows_bad(P.cu_q, g.b, P.Tq) || seq_rows_bad(P.cu_k, g.b, P.Tk)))
-            report_error(P.err, ISPA_ERR_INVALID_ARG, g.b);
-          const int end0 = seg_end(cost, g, 0), end1 = seg_end(cost, g, 1), end = max(end0, end1);
-          if (end == g.j0) continue;  // no key in sight: nothing to load
+        while (ok) {
+          const PromptSeg *g = seg_wait();
+          if (!g || g->mode < 0) break;
+          const int j0 = g->j0, end = max(g->end[0], g->end[1]), h = g->h, k_row = g->k_row, q_row = g->q_row;
+          seg_done();
+          if (end == j0) continue;  // no key in sight: nothing to load
           ok = wait_parity(&sm.q_empty, (n_q & 1) ^ 1, P.err, abort, 52);
           if (!ok) break;
-          const int rows = P.G * P.TQ;
-          mbar_arrive_expect_tx(&sm.q_full, 2 * C::HALVES * rows * 128);
+          mbar_arrive_expect_tx(&sm.q_full, 2 * C::HALVES * P.G * P.TQ * 128);
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int f = 0; f < C::HALVES; ++f)
-              tma_load_5d(sm.q[w] + f * kBox, &tq, &sm.q_full, 0, 0, g.s.q0 + (g.pair * 2 + w) * P.TQ, f, g.h);
+              tma_load_5d(sm.q[w] + f * kBox, &tq, &sm.q_full, 0, 0, q_row + w * P.TQ, f, h);
           ++n_q;
-          for (int j = g.j0; ok && j < end; ++j) {
-            ok = load(&tk, g.s.k0 + j * kTile, g.h);
-            if (ok) ok = load(&tv, g.s.k0 + j * kTile, g.h);
+          for (int j = j0; ok && j < end; ++j) {
+            ok = load(&tk, k_row + j * kTile, h);
+            if (ok) ok = load(&tv, k_row + j * kTile, h);
           }
         }
         if (*abort) {  // let copies in flight land before the CTA exits
@@ -376,9 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(&sm.s_full[w]);
       };
-      while (ok && walk.next(cost, P.B, g)) {
-        const int end0 = seg_end(cost, g, 0), end1 = seg_end(cost, g, 1), end = max(end0, end1);
-        if (end == g.j0) continue;
+      while (ok) {
+        const PromptSeg *g = seg_wait();
+        if (!__all_sync(0xffffffffu, g != nullptr) || g->mode < 0) break;
+        const int j0 = g->j0, end0 = g->end[0], end1 = g->end[1], end = max(end0, end1), len = g->len;
+        // keys that the rows of each tile see at most
+        const int lim0 = P.causal ? g->lim + min(P.TQ, g->n_tok) - 1 : len;
+        const int lim1 = P.causal ? g->lim + min(2 * P.TQ, g->n_tok) - 1 : len;
+        __syncwarp();
+        if (lane == 0) seg_done();
+        else ++n_seg;
+        if (end == j0) continue;
         ok = wait_parity(&sm.q_full, n_q & 1, P.err, abort, 53) && ring_wait(n_ring, 54);
         ++n_q;
         ok = __all_sync(0xffffffffu, ok);
@@ -386,12 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t kn = n_ring;  // ring number of the K tile whose S was issued last
         if (lane == 0) {
-          if (g.j0 < end0) issue_s(0, kn);
-          if (g.j0 < end1) issue_s(1, kn);
+          if (j0 < end0) issue_s(0, kn);
+          if (j0 < end1) issue_s(1, kn);
           mma_commit(&sm.empty[kn % C::STAGES]);
-          if (end == g.j0 + 1) mma_commit(&sm.q_empty);
+          if (end == j0 + 1) mma_commit(&sm.q_empty);
         }
-        for (int j = g.j0; j < end; ++j) {
+        for (int j = j0; j < end; ++j) {
           const uint32_t vn = n_ring + 1;
           kn = n_ring + 2;
           n_ring += 2;
@@ -399,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && j + 1 < end) ok = ring_wait(kn, 56);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const int left = g.s.len - j * kTile;  // keys of the sequence in this tile
+          const int left = len - j * kTile;  // keys of the sequence in this tile
           if (left < kTile && (left & 15)) {
             // rows left .. the end of their 16-key step belong to the next sequence
             uint8_t *v = sm.ring[vn % C::STAGES];
@@ -419,17 +470,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
-              const int seen = min(kTile, cost.limit(g.s, (g.pair * 2 + w + 1) * P.TQ) - j * kTile);
+              const int seen = min(kTile, (w ? lim1 : lim0) - j * kTile);
               const int k_steps = (seen + 15) >> 4;
               const uint64_t vd = dring_v + (uint64_t)(((vn % C::STAGES) * C::TILE) >> 4);
               const uint32_t a_p = tmem + kColS + w * 128, d_o = tmem + kColO + w * 128;
               if (k_steps == 8) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > g.j0 || kk > 0) ? 1u : 0u);
+                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > j0 || kk > 0) ? 1u : 0u);
               } else {
                 for (int kk = 0; kk < k_steps; ++kk)
-                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > g.j0 || kk > 0) ? 1u : 0u);
+                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > j0 || kk > 0) ? 1u : 0u);
               }
               if (j + 1 < my_end)
                 issue_s(w, kn);
@@ -453,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int w = (warp >> 2) - 1;
     const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
     const int tok = r / P.G, head = r % P.G;
@@ -461,38 +511,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t col_s = lane_base + kColS + w * 128, col_o = lane_base + kColO + w * 128;
     uint32_t n_s = 0, n_o = 0;
     bool ok = true;
-    while (ok && walk.next(cost, P.B, g)) {
-      const int qi = (g.pair * 2 + w) * P.TQ + tok;  // this row's token in its sequence
-      const bool row_ok = tok < P.TQ && qi < g.s.n;
-      const int lim = P.causal ? g.s.past + qi + 1 : g.s.len;
-      const int lim_first = P.causal ? g.s.past + (g.pair * 2 + w) * P.TQ + 1 : g.s.len;
-      const int end = seg_end(cost, g, w);
+    while (ok) {
+      const PromptSeg *g = seg_wait();
+      if (!__all_sync(0xffffffffu, g != nullptr) || g->mode < 0) break;
+      const int t = w * P.TQ + tok;  // this row's token in the pair
+      const bool row_ok = tok < P.TQ && t < g->n_tok;
+      const int lim = P.causal ? g->lim + t : g->len;
+      const int lim_first = P.causal ? g->lim + w * P.TQ : g->len;
+      const int j0 = g->j0, end = g->end[w], mode = g->mode, slot = 2 * blockIdx.x + g->slot;
+      const long long out = (long long)(g->q_row + (row_ok ? t : 0)) * P.H + g->h * P.G + head;
+      __syncwarp();
+      if (lane == 0) seg_done();
+      else ++n_seg;
       float m_ref = 0.f, l = 0.f;
-      for (int j = g.j0; j < end; ++j) {
+      for (int j = j0; j < end; ++j) {
         ok = wait_parity_spin(&sm.s_full[w], n_s & 1, P.err, abort, 61 + w);
         ++n_s;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[4][32];
+        // S is read twice, 32 columns at a time, instead of being held in 128 registers
+        const bool edge = (j + 1) * kTile > lim_first;  // the diagonal, or the sequence's end
+        const int valid = lim - j * kTile;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t sr[2][32];
+        tmem_ld32(col_s, sr[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(col_s + c * 32, sr[c]);
-        tmem_wait_ld();
-        if ((j + 1) * kTile > lim_first) {  // the diagonal, or the sequence's end
-          const int valid = lim - j * kTile;
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld();
+          if (c < 3) tmem_ld32(col_s + (c + 1) * 32, sr[(c + 1) & 1]);
+          uint32_t(&x)[32] = sr[c & 1];
+          if (edge) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= valid) sr[c >> 5][c & 31] = 0xff800000u;
+            for (int t = 0; t < 32; ++t)
+              if (c * 32 + t >= valid) x[t] = 0xff800000u;
+          }
+#pragma unroll
+          for (int t = 0; t < 32; t += 2)
+            mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(x[t]), __uint_as_float(x[t + 1]));
         }
-        float mx[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) mx[t] = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 2)
-          mx[(c >> 1) & 7] = max3(mx[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
-                                  __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-        const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * P.scale_log2;
-        if (j == g.j0) {
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale_log2;
+        tmem_ld32(col_s, sr[0]);
+        if (j == j0) {
           m_ref = mt == -INFINITY ? 0.f : mt;
         } else if (__any_sync(0xffffffffu, mt > m_ref + kThreshold)) {
           const float m_new = fmaxf(m_ref, mt);
@@ -515,15 +575,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld();
+          if (c < 3) tmem_ld32(col_s + (c + 1) * 32, sr[(c + 1) & 1]);
+          uint32_t(&y)[32] = sr[c & 1];
+          if (edge) {
+#pragma unroll
+            for (int t = 0; t < 32; ++t)
+              if (c * 32 + t >= valid) y[t] = 0xff800000u;
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int t = 0; t < 16; ++t) {
-            const float2 x =
-                fma2(make_float2(__uint_as_float(sr[c][2 * t]), __uint_as_float(sr[c][2 * t + 1])), sc2, nm2);
+            const float2 x = fma2(make_float2(__uint_as_float(y[2 * t]), __uint_as_float(y[2 * t + 1])), sc2, nm2);
             const float2 pp = make_float2(exp2_fast(x.x), exp2_fast(x.y));
             ls[t & 1] = add2(ls[t & 1], pp);
             pk[t] = pack2<T>(pp.x, pp.y);
           }
+          // columns [16 c, 16 c + 16) of P: their scores (chunk c / 2) have been read
           tmem_st16(col_s + c * 16, pk);
         }
         tmem_wait_st();
@@ -533,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the segment's output
-      if (end > g.j0) {
+      if (end > j0) {
         ok = wait_parity(&sm.o_final[w], n_o & 1, P.err, abort, 63 + w);
         ++n_o;
         ok = __all_sync(0xffffffffu, ok);
@@ -541,14 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const bool some = l > 0.f;
-      if (g.whole()) {
-        const long long out = ((long long)(g.s.q0 + (row_ok ? qi : 0)) * P.H + g.h * P.G + head);
+      if (mode == 1) {
         const float inv = some ? 1.f / l : 0.f;
         TO *dst = static_cast<TO *>(P.o) + out * D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t raw[32];
-          if (end > g.j0) {
+          if (end > j0) {
             tmem_ld32(col_o + c * 32, raw);
             tmem_wait_ld();
           }
@@ -563,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row_ok && P.lse) P.lse[out] = some ? (m_ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
       } else {
-        const int slot = 2 * blockIdx.x + (g.j0 == 0 ? 1 : 0);
         float *part = P.part + ((size_t)slot * 2 + w) * tile_floats<D>();
         part[r] = some ? m_ref : -INFINITY;
         part[kTile + r] = l;
@@ -571,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t raw[32];
-          if (end > g.j0) {
+          if (end > j0) {
             tmem_ld32(col_o + c * 32, raw);
             tmem_wait_ld();
           }
@@ -581,12 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 some ? make_float4(__uint_as_float(raw[4 * v]), __uint_as_float(raw[4 * v + 1]),
                                    __uint_as_float(raw[4 * v + 2]), __uint_as_float(raw[4 * v + 3]))
                      : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (w == 0 && r == 0) {
-          PartMeta *m = P.meta + slot;
-          m->b = g.b;
-          m->item = g.h * g.s.pairs + g.pair;
-          m->state = g.j1 == g.total ? 2 : 1;
         }
       }
       tc_fence_before();  // O is read before the p_full that lets the next item overwrite it

@@ -33,10 +33,6 @@ struct RowParams {
   int *err;
 };
 
-__device__ __forceinline__ void report_seq(int *err, int b) {
-  if (atomicCAS(err, 0, ISPA_ERR_INVALID_ARG) == 0) atomicExch(err + 1, b);
-}
-
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));

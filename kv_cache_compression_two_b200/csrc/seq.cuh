@@ -32,6 +32,11 @@ __device__ __forceinline__ bool seq_rows_bad(const int *cu, int b, int T) {
   return c0 < 0 || c1 < c0 || c1 > T;
 }
 
+// Records a value of sequence b that is out of range (err: the device error word).
+__device__ __forceinline__ void report_seq(int *err, int b) {
+  if (atomicCAS(err, 0, ISPA_ERR_INVALID_ARG) == 0) atomicExch(err + 1, b);
+}
+
 __device__ __forceinline__ int seq_len(const int *lens, int b, int cap) {
   return min(max(__ldg(lens + b), 0), cap);
 }
