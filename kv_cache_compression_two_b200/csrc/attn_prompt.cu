@@ -170,7 +170,8 @@ struct PromptWalk {
     pair = s.pairs ? r.tag % s.pairs : 0;
     j = (int)(r.off - r.begin);
   }
-  __device__ bool next(const PromptCost &c, int B, PromptSeg &g, PartMeta *meta) {
+  // (not inlined, with its state in shared memory: its registers would be taken from the roles' loops)
+  __device__ __noinline__ bool next(const PromptCost &c, int B, PromptSeg &g, PartMeta *meta) {
     if (left <= 0) return false;
     int total = pair < s.pairs ? c.steps(s, pair) : 0;
     while (j >= total) {  // on to the next item that has steps
@@ -231,6 +232,7 @@ struct PromptSmem {
   uint64_t drain;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   PromptSeg seg[kSegs];
+  PromptWalk walk;
   long long scratch[kThreads / 32 + 6];
   SplitRange range;
   uint32_t tmem_base;
@@ -273,6 +275,43 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// MMAs issued from warp-uniform code: every lane executes the statement with the
+// same operands and the elected one issues, so that descriptors and addresses stay in
+// uniform registers (inside an `if (lane == 0)` each of them had to be moved there,
+// about 100 cycles an MMA beside two busy softmax warps).  Descriptors are given by
+// their low words; the high word (stride 1024, version 1, 128-byte swizzle) is constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss_u(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                         uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%2, %6};\n\tmov.b64 db, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %4, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_u(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                         uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], db, %4, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_u(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int y, int z, int w,
                                             int v) {
   asm volatile(
@@ -291,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   PromptSmem<D> &sm =
       *reinterpret_cast<PromptSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int *abort = &sm.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const PromptCost cost = {P.cu_q, P.cu_k, P.Tq, P.Tk, P.TQ, P.H_kv, P.causal};
 
   if (threadIdx.x == 0) {
@@ -327,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
   // item i of the stretch, for the roles: seg_wait, read, seg_done
   uint32_t n_seg = 0;
   auto seg_wait = [&]() -> const PromptSeg * {
@@ -343,15 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
       // ---------------------------------------------------------- scheduler
       if (lane == 0) {
-        PromptWalk walk;
-        walk.start(cost, sm.range);
+        sm.walk.start(cost, sm.range);
         for (bool more = true; more; ++n_seg) {
           const uint32_t i = n_seg % kSegs;
           if (!wait_parity(&sm.seg_empty[i], ((n_seg / kSegs) & 1) ^ 1, P.err, abort, 49)) break;
-          PromptSeg g;
-          more = walk.next(cost, P.B, g, P.meta + 2 * blockIdx.x);
-          if (!more) g.mode = -1;
-          sm.seg[i] = g;
+          more = sm.walk.next(cost, P.B, sm.seg[i], P.meta + 2 * blockIdx.x);
+          if (!more) sm.seg[i].mode = -1;
           mbar_arrive(&sm.seg_full[i]);
         }
       }
@@ -398,106 +434,116 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      constexpr int fmt = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0 : 1;
+      constexpr int fmt = std::is_same<T, __half>::value ? 0 : 1;
       constexpr uint32_t idesc_s = make_idesc(128, 128, fmt, 0, 0);   // Q (K-major) x K (K-major)
       constexpr uint32_t idesc_pv = make_idesc(128, D, fmt, 0, 1);    // P (TMEM) x V (MN-major)
-      const uint64_t dq0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-      const uint64_t dring_k = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
-      const uint64_t dring_v = smem_desc_sw128(smem_u32(sm.ring[0]), kBox, 1024);
-      uint32_t n_ring = 0, n_q = 0, n_p[2] = {0, 0};
+      const uint32_t leader = elect_one();
+      const uint32_t dq = ((smem_u32(sm.q[0]) >> 4) & 0x3fffu) | (1u << 16);
+      const uint32_t dk = ((smem_u32(sm.ring[0]) >> 4) & 0x3fffu) | (1u << 16);
+      const uint32_t dv = ((smem_u32(sm.ring[0]) >> 4) & 0x3fffu) | ((uint32_t)(kBox >> 4) << 16);
+      uint32_t st = 0, ph = 0;    // ring stage of the next tile to be consumed, and its phase
+      uint32_t n_q = 0, ph_p = 0;  // phases of q_full and, one bit a tile, of p_full
       bool ok = true;
-      auto ring_wait = [&](uint32_t k, int site) {
-        return wait_parity(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, P.err, abort, site);
+      auto advance = [&](uint32_t &s, uint32_t &p) {
+        if (++s == C::STAGES) {
+          s = 0;
+          p ^= 1;
+        }
       };
-      auto issue_s = [&](int w, uint32_t k) {
-        const uint64_t qd = dq0 + (uint64_t)((w * C::TILE) >> 4);
-        const uint64_t kd = dring_k + (uint64_t)(((k % C::STAGES) * C::TILE) >> 4);
+      auto issue_s = [&](int w, uint32_t stage) {
+        const uint32_t qd = dq + ((w * C::TILE) >> 4), kd = dk + stage * (C::TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
-          mma_ss(tmem + kColS + w * 128, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u, 0);
+          const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+          mma_ss_u(leader, tmem + kColS + w * 128, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
         }
-        mma_commit(&sm.s_full[w]);
+        mma_commit_u(leader, &sm.s_full[w]);
       };
-      while (ok) {
+      while (true) {
         const PromptSeg *g = seg_wait();
-        if (!__all_sync(0xffffffffu, g != nullptr) || g->mode < 0) break;
-        const int j0 = g->j0, end0 = g->end[0], end1 = g->end[1], end = max(end0, end1), len = g->len;
+        ok = __all_sync(0xffffffffu, g != nullptr);
+        if (!ok) break;
+        // (through a shuffle: uniform for the compiler too)
+        auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        const int mode = uni(g->mode), j0 = uni(g->j0), end0 = uni(g->end[0]), end1 = uni(g->end[1]);
+        const int len = uni(g->len), n_tok = uni(g->n_tok), lim = uni(g->lim);
+        if (mode < 0) break;
+        const int end = max(end0, end1);
         // keys that the rows of each tile see at most
-        const int lim0 = P.causal ? g->lim + min(P.TQ, g->n_tok) - 1 : len;
-        const int lim1 = P.causal ? g->lim + min(2 * P.TQ, g->n_tok) - 1 : len;
-        __syncwarp();
+        const int lim0 = P.causal ? lim + min(P.TQ, n_tok) - 1 : len;
+        const int lim1 = P.causal ? lim + min(2 * P.TQ, n_tok) - 1 : len;
         if (lane == 0) seg_done();
         else ++n_seg;
+        __syncwarp();
         if (end == j0) continue;
-        ok = wait_parity(&sm.q_full, n_q & 1, P.err, abort, 53) && ring_wait(n_ring, 54);
-        ++n_q;
+        ok = wait_parity(&sm.q_full, n_q, P.err, abort, 53) && wait_parity(&sm.full[st], ph, P.err, abort, 54);
+        n_q ^= 1;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t kn = n_ring;  // ring number of the K tile whose S was issued last
-        if (lane == 0) {
-          if (j0 < end0) issue_s(0, kn);
-          if (j0 < end1) issue_s(1, kn);
-          mma_commit(&sm.empty[kn % C::STAGES]);
-          if (end == j0 + 1) mma_commit(&sm.q_empty);
-        }
+        if (j0 < end0) issue_s(0, st);
+        if (j0 < end1) issue_s(1, st);
+        mma_commit_u(leader, &sm.empty[st]);
+        if (end == j0 + 1) mma_commit_u(leader, &sm.q_empty);
+        advance(st, ph);
+#pragma unroll 1
         for (int j = j0; j < end; ++j) {
-          const uint32_t vn = n_ring + 1;
-          kn = n_ring + 2;
-          n_ring += 2;
-          ok = ring_wait(vn, 55);
-          if (ok && j + 1 < end) ok = ring_wait(kn, 56);
+          const uint32_t sv = st;
+          ok = wait_parity(&sm.full[st], ph, P.err, abort, 55);
+          advance(st, ph);
+          const uint32_t sk = st;
+          if (j + 1 < end) {
+            if (ok) ok = wait_parity(&sm.full[st], ph, P.err, abort, 56);
+            advance(st, ph);
+          }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int left = len - j * kTile;  // keys of the sequence in this tile
           if (left < kTile && (left & 15)) {
             // rows left .. the end of their 16-key step belong to the next sequence
-            uint8_t *v = sm.ring[vn % C::STAGES];
+            uint8_t *v = sm.ring[sv];
             const int n16 = (16 - (left & 15)) * 8;
             for (int i = lane; i < n16 * C::HALVES; i += 32)
               *reinterpret_cast<uint4 *>(v + (i / n16) * kBox + left * 128 + (i % n16) * 16) = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
+          const uint32_t vd = dv + sv * (C::TILE >> 4);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const int my_end = w ? end1 : end0;
-            if (j >= my_end) continue;
-            ok = wait_parity_spin(&sm.p_full[w], n_p[w] & 1, P.err, abort, 57 + w);
-            ++n_p[w];
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const int seen = min(kTile, (w ? lim1 : lim0) - j * kTile);
-              const int k_steps = (seen + 15) >> 4;
-              const uint64_t vd = dring_v + (uint64_t)(((vn % C::STAGES) * C::TILE) >> 4);
+            if (j < my_end) {
+              ok = wait_parity(&sm.p_full[w], (ph_p >> w) & 1, P.err, abort, 57 + w);
+              ph_p ^= 1u << w;
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+              const int k_steps = (min(kTile, (w ? lim1 : lim0) - j * kTile) + 15) >> 4;
               const uint32_t a_p = tmem + kColS + w * 128, d_o = tmem + kColO + w * 128;
               if (k_steps == 8) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > j0 || kk > 0) ? 1u : 0u);
+                  mma_ts_u(leader, d_o, a_p + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || j > j0 ? 1u : 0u);
               } else {
+#pragma unroll 1
                 for (int kk = 0; kk < k_steps; ++kk)
-                  mma_ts(d_o, a_p + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), idesc_pv, (j > j0 || kk > 0) ? 1u : 0u);
+                  mma_ts_u(leader, d_o, a_p + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || j > j0 ? 1u : 0u);
               }
               if (j + 1 < my_end)
-                issue_s(w, kn);
+                issue_s(w, sk);
               else
-                mma_commit(&sm.o_final[w]);
+                mma_commit_u(leader, &sm.o_final[w]);
             }
           }
           if (!ok) break;
-          if (lane == 0) {
-            mma_commit(&sm.empty[vn % C::STAGES]);
-            if (j + 1 < end) mma_commit(&sm.empty[kn % C::STAGES]);
-            if (j + 2 == end) mma_commit(&sm.q_empty);
-          }
+          mma_commit_u(leader, &sm.empty[sv]);
+          if (j + 1 < end) mma_commit_u(leader, &sm.empty[sk]);
+          if (j + 2 == end) mma_commit_u(leader, &sm.q_empty);
         }
+        if (!ok) break;
       }
-      if (!ok && lane == 0) {
-        mma_commit(&sm.drain);
+      if (!ok) {
+        mma_commit_u(leader, &sm.drain);
         wait_parity_drain(&sm.drain, 0, P.err);
       }
       __syncwarp();
@@ -525,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       else ++n_seg;
       float m_ref = 0.f, l = 0.f;
       for (int j = j0; j < end; ++j) {
-        ok = wait_parity_spin(&sm.s_full[w], n_s & 1, P.err, abort, 61 + w);
+        ok = wait_parity(&sm.s_full[w], n_s & 1, P.err, abort, 61 + w);
         ++n_s;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
