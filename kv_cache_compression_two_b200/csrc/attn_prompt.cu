@@ -49,12 +49,12 @@ namespace ispa {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kTile = 128;
 constexpr int kBox = 128 * 128;  // bytes of 128 rows x 64 columns
 constexpr int kMinPart = 4;
 constexpr int kSegs = 4;         // items handed on ahead
-constexpr int kSegReaders = 10;  // producer, issuer, eight softmax warps
+constexpr int kSegReaders = 18;  // producer, issuer, sixteen softmax warps
 constexpr float kThreshold = 8.0f;  // the reference maximum moves when passed by more than this (log2)
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -228,9 +228,10 @@ struct PromptSmem {
   uint8_t ring[Cfg<D>::STAGES][Cfg<D>::TILE];
   uint64_t full[Cfg<D>::STAGES], empty[Cfg<D>::STAGES];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_final[2], swapped[2];
   uint64_t drain;
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+  float swap[2][2][kTile];  // per tile: what the two threads of a row tell each other
   PromptSeg seg[kSegs];
   PromptWalk walk;
   long long scratch[kThreads / 32 + 6];
@@ -326,9 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, PromptParams P) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  PromptSmem<D> &sm =
-      *reinterpret_cast<PromptSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  PromptSmem<D> &sm = *reinterpret_cast<PromptSmem<D> *>(smem_raw);
+  if (smem_u32(smem_raw) & 1023u) {  // the operand tiles need it; nothing static lies in front
+    if (threadIdx.x == 0) report_error(P.err, ISPA_ERR_CUDA, 48);
+    return;
+  }
   volatile int *abort = &sm.abort;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const PromptCost cost = {P.cu_q, P.cu_k, P.Tq, P.Tk, P.TQ, P.H_kv, P.causal};
@@ -342,7 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.q_empty, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sm.s_full[w], 1);
-      mbar_init(&sm.p_full[w], 128);
+      mbar_init(&sm.p_half[w], 8);
+      mbar_init(&sm.p_full[w], 8);
+      mbar_init(&sm.swapped[w], 8);
       mbar_init(&sm.o_final[w], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < P.B; b += kThreads)
       if (seq_rows_bad(P.cu_q, b, P.Tq) || seq_rows_bad(P.cu_k, b, P.Tk)) report_error(P.err, ISPA_ERR_INVALID_ARG, b);
-  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 17) tmem_alloc(&sm.tmem_base, 512);
   split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kMinPart, &sm.range, sm.scratch);
   tc_fence_before();
   __syncthreads();
@@ -378,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++n_seg;
   };
 
-  if (warp < 4) {
-    if (warp == 2) {
+  if (warp >= 16) {
+    if (warp == 18) {
       // ---------------------------------------------------------- scheduler
       if (lane == 0) {
         sm.walk.start(cost, sm.range);
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sm.seg_full[i]);
         }
       }
-    } else if (warp == 0) {
+    } else if (warp == 16) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
         uint32_t n_ring = 0, pend = 0, ph_bits = 0, n_q = 0;
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n_q) wait_parity_drain(&sm.q_full, (n_q - 1) & 1, P.err);
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == 17) {
       // ---------------------------------------------------------- MMA issuer
       constexpr int fmt = std::is_same<T, __half>::value ? 0 : 1;
       constexpr uint32_t idesc_s = make_idesc(128, 128, fmt, 0, 0);   // Q (K-major) x K (K-major)
@@ -513,22 +519,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int w = 0; w < 2; ++w) {
             const int my_end = w ? end1 : end0;
             if (j < my_end) {
-              ok = wait_parity(&sm.p_full[w], (ph_p >> w) & 1, P.err, abort, 57 + w);
-              ph_p ^= 1u << w;
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              tc_fence_after();
               const int k_steps = (min(kTile, (w ? lim1 : lim0) - j * kTile) + 15) >> 4;
               const uint32_t a_p = tmem + kColS + w * 128, d_o = tmem + kColO + w * 128;
-              if (k_steps == 8) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  mma_ts_u(leader, d_o, a_p + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || j > j0 ? 1u : 0u);
-              } else {
-#pragma unroll 1
-                for (int kk = 0; kk < k_steps; ++kk)
-                  mma_ts_u(leader, d_o, a_p + kk * 8, vd + kk * (2048 >> 4), idesc_pv, kk > 0 || j > j0 ? 1u : 0u);
+              for (int part = 0; part < 2; ++part) {  // the weights come in two parts: 16-key steps 0 1 4 5, then 2 3 6 7
+                ok = wait_parity(part ? &sm.p_full[w] : &sm.p_half[w], (ph_p >> w) & 1, P.err, abort, 57 + w);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int kk = (i >> 1) * 4 + part * 2 + (i & 1);
+                  if (kk < k_steps)
+                    mma_ts_u(leader, d_o, a_p + kk * 8 + (kk >> 2) * 32, vd + kk * (2048 >> 4), idesc_pv,
+                             kk > 0 || j > j0 ? 1u : 0u);
+                }
               }
+              ph_p ^= 1u << w;
+              if (!ok) break;
               if (j + 1 < my_end)
                 issue_s(w, sk);
               else
@@ -550,12 +558,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and output
-    const int w = (warp >> 2) - 1;
+    const int w = warp >> 3, half = (warp >> 2) & 1;
     const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
     const int tok = r / P.G, head = r % P.G;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t col_s = lane_base + kColS + w * 128, col_o = lane_base + kColO + w * 128;
-    uint32_t n_s = 0, n_o = 0;
+    const uint32_t col_s = lane_base + kColS + w * 128 + half * 64;        // this thread's 64 scores
+    const uint32_t col_o = lane_base + kColO + w * 128 + half * (D / 2);   // and its half of O
+    float *mine = &sm.swap[w][half][r], *theirs = &sm.swap[w][half ^ 1][r];
+    uint32_t n_s = 0, n_o = 0, n_x = 0;
+    auto swap_sync = [&]() {  // the tile's eight warps; bounded like every wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.swapped[w]);
+      const bool ok = wait_parity(&sm.swapped[w], n_x & 1, P.err, abort, 65 + w);
+      ++n_x;
+      return (bool)__all_sync(0xffffffffu, ok);
+    };
     bool ok = true;
     while (ok) {
       const PromptSeg *g = seg_wait();
@@ -576,17 +593,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // S is read twice, 32 columns at a time, instead of being held in 128 registers
+        // the scores are read twice, 32 columns at a time: registers are scarcer than that bandwidth
         const bool edge = (j + 1) * kTile > lim_first;  // the diagonal, or the sequence's end
-        const int valid = lim - j * kTile;
+        const int valid = lim - j * kTile - half * 64;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t sr[2][32];
-        tmem_ld32(col_s, sr[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          tmem_ld32(col_s + c * 32, x);
           tmem_wait_ld();
-          if (c < 3) tmem_ld32(col_s + (c + 1) * 32, sr[(c + 1) & 1]);
-          uint32_t(&x)[32] = sr[c & 1];
           if (edge) {
 #pragma unroll
             for (int t = 0; t < 32; ++t)
@@ -596,8 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 32; t += 2)
             mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(x[t]), __uint_as_float(x[t + 1]));
         }
-        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale_log2;
-        tmem_ld32(col_s, sr[0]);
+        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        *mine = mt;
+        ok = swap_sync();
+        if (!ok) break;
+        mt = fmaxf(mt, *theirs) * P.scale_log2;
         if (j == j0) {
           m_ref = mt == -INFINITY ? 0.f : mt;
         } else if (__any_sync(0xffffffffu, mt > m_ref + kThreshold)) {
@@ -606,44 +624,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = m_new;
           l *= f;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(col_o + c * 32, o);
+          for (int c = 0; c < D / 2; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(col_o + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
-            tmem_st16(col_o + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-            tmem_st16(col_o + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+            for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
+            tmem_st16(col_o + c, o);
           }
         }
         // P = 2^(s scale log2e - m_ref) <= 2^8 in the input type, over the first 64 columns of S
         const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t y[32], pk[16];
+          tmem_ld32(col_s + c * 32, y);
           tmem_wait_ld();
-          if (c < 3) tmem_ld32(col_s + (c + 1) * 32, sr[(c + 1) & 1]);
-          uint32_t(&y)[32] = sr[c & 1];
           if (edge) {
 #pragma unroll
             for (int t = 0; t < 32; ++t)
               if (c * 32 + t >= valid) y[t] = 0xff800000u;
           }
-          uint32_t pk[16];
 #pragma unroll
           for (int t = 0; t < 16; ++t) {
-            const float2 x = fma2(make_float2(__uint_as_float(y[2 * t]), __uint_as_float(y[2 * t + 1])), sc2, nm2);
+            const float2 x =
+                fma2(make_float2(__uint_as_float(y[2 * t]), __uint_as_float(y[2 * t + 1])), sc2, nm2);
             const float2 pp = make_float2(exp2_fast(x.x), exp2_fast(x.y));
             ls[t & 1] = add2(ls[t & 1], pp);
             pk[t] = pack2<T>(pp.x, pp.y);
           }
-          // columns [16 c, 16 c + 16) of P: their scores (chunk c / 2) have been read
-          tmem_st16(col_s + c * 16, pk);
+          tmem_st16(col_s + c * 16, pk);  // over scores that have been read
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c == 0 ? &sm.p_half[w] : &sm.p_full[w]);
         }
-        tmem_wait_st();
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-        tc_fence_before();
-        mbar_arrive(&sm.p_full[w]);
       }
       if (!ok) break;
       // ---- the segment's output
@@ -653,43 +670,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        *mine = l;
+        ok = swap_sync();
+        if (!ok) break;
+        l += *theirs;
+        ok = swap_sync();  // read before the next item's first maximum takes its place
+        if (!ok) break;
       }
       const bool some = l > 0.f;
       if (mode == 1) {
         const float inv = some ? 1.f / l : 0.f;
-        TO *dst = static_cast<TO *>(P.o) + out * D;
+        TO *dst = static_cast<TO *>(P.o) + out * D + half * (D / 2);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t raw[32];
+        for (int c = 0; c < D / 2; c += 16) {
+          uint32_t raw[16];
           if (end > j0) {
-            tmem_ld32(col_o + c * 32, raw);
+            tmem_ld16(col_o + c, raw);
             tmem_wait_ld();
           }
           if (!row_ok) continue;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
+          for (int v = 0; v < 2; ++v) {
             float x[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) x[t] = some ? __uint_as_float(raw[8 * v + t]) * inv : 0.f;
-            store8(dst + c * 32 + v * 8, x);
+            store8(dst + c + v * 8, x);
           }
         }
-        if (row_ok && P.lse) P.lse[out] = some ? (m_ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+        if (row_ok && half == 0 && P.lse) P.lse[out] = some ? (m_ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
       } else {
         float *part = P.part + ((size_t)slot * 2 + w) * tile_floats<D>();
-        part[r] = some ? m_ref : -INFINITY;
-        part[kTile + r] = l;
-        float4 *po = reinterpret_cast<float4 *>(part + 2 * kTile);
+        if (half == 0) {
+          part[r] = some ? m_ref : -INFINITY;
+          part[kTile + r] = l;
+        }
+        float4 *po = reinterpret_cast<float4 *>(part + 2 * kTile) + half * (D / 8) * kTile + r;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t raw[32];
+        for (int c = 0; c < D / 2; c += 16) {
+          uint32_t raw[16];
           if (end > j0) {
-            tmem_ld32(col_o + c * 32, raw);
+            tmem_ld16(col_o + c, raw);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            po[(c * 8 + v) * kTile + r] =
+          for (int v = 0; v < 4; ++v)
+            po[(c / 4 + v) * kTile] =
                 some ? make_float4(__uint_as_float(raw[4 * v]), __uint_as_float(raw[4 * v + 1]),
                                    __uint_as_float(raw[4 * v + 2]), __uint_as_float(raw[4 * v + 3]))
                      : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -700,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of the item that slot 2c + 1 starts: block (c, tile, 32 columns), one row per thread.
@@ -749,7 +774,8 @@ template <int D, typename T, typename TO>
 ispa_status launch_one(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PromptParams &P,
                        cudaStream_t s) {
   auto kern = attn_prompt_kernel<D, T, TO>;
-  constexpr int smem = sizeof(PromptSmem<D>) + 1024;
+  constexpr int smem = sizeof(PromptSmem<D>);
+  static_assert(smem <= 232448, "shared memory of a block");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_status(e, "attn_prompt shared memory");
   kern<<<P.nc, kThreads, smem, s>>>(tq, tk, tv, P);
