@@ -402,133 +402,161 @@ def ispa_selftest_wait_timeout(wait_ns: int, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # Sequences: the quantised paged cache and attention over packed prompts
 # ---------------------------------------------------------------------------
-class _Seq:
-    """One sequence call's view of its tensors: all on the current device, contents and shapes checked."""
+# A decoding step's calls take a few microseconds on the device, so their checks
+# are kept to a few attribute reads a tensor; _explain says what was wrong.
+_seq_env = None
 
-    def __init__(self):
+
+def _seq():
+    """(int32, uint8, float32, dtype codes, current device, raw current stream of a device), looked up once."""
+    global _seq_env
+    if _seq_env is None:
         import torch
-        self.torch = torch
-        self.dev = torch.cuda.current_device()
-        self.ints, self.bytes_, self.f32 = torch.int32, torch.uint8, torch.float32
-        self.code = {torch.bfloat16: ISPA_BF16, torch.float16: ISPA_F16, torch.float32: ISPA_F32}
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _seq_env = (torch.int32, torch.uint8, torch.float32,
+                    {torch.bfloat16: ISPA_BF16, torch.float16: ISPA_F16, torch.float32: ISPA_F32},
+                    torch.cuda.current_device, raw)
+    return _seq_env
 
-    def ptr(self, x, name, dtype, shape):
-        """A contiguous tensor of this dtype; shape entries that are None may have any size."""
-        if not isinstance(x, self.torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if x.dtype != dtype:
-            raise ValueError(f"{name}: dtype {x.dtype}, expected {dtype}")
-        if x.get_device() != self.dev:
-            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{self.dev}")
-        have = x.shape
-        if len(have) != len(shape) or any(w is not None and w != h for w, h in zip(shape, have)):
-            raise ValueError(f"{name}: shape {tuple(have)}, expected {shape}")
-        if not x.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-        return x.data_ptr()
 
-    def rows(self, x, name, heads, d, dtype=None):
-        """Packed rows [T, heads, d] whose tokens may be strided: (pointer, T, stride, dtype code)."""
-        if not isinstance(x, self.torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        code = self.code.get(x.dtype)
-        if code is None or code == ISPA_F32 or (dtype is not None and code != dtype):
-            raise ValueError(f"{name}: dtype {x.dtype} does not fit the call")
-        if x.get_device() != self.dev:
-            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{self.dev}")
-        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d:
-            raise ValueError(f"{name}: shape {tuple(x.shape)}, expected [T, {heads}, {d}]")
-        T, stride = x.shape[0], x.stride()
-        if T <= 1:
-            step = heads * d
-        else:
-            step = stride[0]
-        if T and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
-            raise ValueError(f"{name}: a row's heads must lie back to back")
-        return x.data_ptr(), T, step, code
+def _explain(x, name, want, shape, dev) -> Exception:
+    import torch
+    if not isinstance(x, torch.Tensor):
+        return TypeError(f"{name}: expected a torch.Tensor")
+    if x.get_device() != dev or dev != _seq()[4]():
+        return ValueError(f"{name}: on {x.device}; every tensor of a call must be on the current device")
+    return ValueError(f"{name}: {x.dtype} {tuple(x.shape)}, strides {x.stride()}; expected {want} {shape}")
 
-    def cache(self, desc, kvq, table, B):
-        need = ispa_kvq_bytes(desc)
-        if need == 0:
-            raise ValueError("desc: not a valid cache layout")
-        if isinstance(kvq, self.torch.Tensor) and kvq.numel() < need:
-            raise ValueError(f"kvq: {kvq.numel()} bytes, the layout needs {need}")
-        return self.ptr(kvq, "kvq", self.bytes_, (None,)), self.ptr(table, "block_table", self.ints, (B, None))
+
+def _flat(x, name, dtype, shape, dev) -> int:
+    """Address of a contiguous tensor of this dtype, shape and device."""
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == dev and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    raise _explain(x, name, dtype, shape, dev)
+
+
+def _rows(x, name, heads, d, code, dev):
+    """Packed rows [T, heads, d] whose tokens may be strided: (address, T, stride)."""
+    try:
+        T, h, c = x.shape
+        if h == heads and c == d and _seq()[3].get(x.dtype, -1) == code != ISPA_F32 and x.get_device() == dev:
+            st, sh, sc = x.stride()
+            if T <= 1:
+                st = heads * d
+            if T == 0 or (sc == 1 and (sh == d or heads == 1)):
+                return x.data_ptr(), T, st
+    except (AttributeError, ValueError):
+        pass
+    raise _explain(x, name, "bf16 or fp16 (one type a call), each row's heads back to back,", f"[T, {heads}, {d}]", dev)
+
+
+def _device(x, name) -> int:
+    """The device of a call's first tensor, which has to be the current one."""
+    try:
+        dev = x.get_device()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
+    if dev < 0 or dev != _seq()[4]():
+        raise ValueError(f"{name}: on {x.device}; every tensor of a call must be on the current device")
+    return dev
+
+
+def _cache(desc, kvq, table, B, dev):
+    """Addresses of the cache and its block table, and the table's width."""
+    env = _seq()
+    need = lib().ispa_kvq_bytes(desc)
+    if need == 0:
+        raise ValueError("desc: not a valid cache layout")
+    n = kvq.numel()
+    if n < need:
+        raise ValueError(f"kvq: {n} bytes, the layout needs {need}")
+    wide = table.shape[-1]
+    return _flat(kvq, "kvq", env[1], (n,), dev), _flat(table, "block_table", env[0], (B, wide), dev), wide
+
+
+def _at(stream, dev):
+    return _seq()[5](dev) if stream is None else _stream(stream)
 
 
 def ispa_kvq_bytes(desc: KvqDesc) -> int:
-    return int(lib().ispa_kvq_bytes(ctypes.byref(desc)))
+    return int(lib().ispa_kvq_bytes(desc))
 
 
 def ispa_kvq_write(desc: KvqDesc, k, v, block_table, seq_lens, cu_new, kvq, stream=None) -> None:
     """Quantises the packed rows k, v [T, H_kv, d] into the cache (seq_lens counts them already)."""
-    s = _Seq()
+    dev, i32 = _device(k, "k"), _seq()[0]
+    code = _seq()[3].get(k.dtype, -1)
     B = seq_lens.shape[0]
-    kp, T, ks, dt = s.rows(k, "k", desc.H_kv, desc.head_dim)
-    vp, Tv, vs, _ = s.rows(v, "v", desc.H_kv, desc.head_dim, dt)
+    kp, T, ks = _rows(k, "k", desc.H_kv, desc.head_dim, code, dev)
+    vp, Tv, vs = _rows(v, "v", desc.H_kv, desc.head_dim, code, dev)
     if T != Tv:
         raise ValueError(f"k has {T} rows, v {Tv}")
-    cp, tp = s.cache(desc, kvq, block_table, B)
-    _check(lib().ispa_kvq_write(ctypes.byref(desc), B, T, tp, block_table.shape[1],
-                                s.ptr(seq_lens, "seq_lens", s.ints, (B,)), s.ptr(cu_new, "cu_new", s.ints, (B + 1,)),
-                                kp, ks, vp, vs, dt, cp, _stream(stream)))
+    cp, tp, wide = _cache(desc, kvq, block_table, B, dev)
+    _check(lib().ispa_kvq_write(desc, B, T, tp, wide, _flat(seq_lens, "seq_lens", i32, (B,), dev),
+                                _flat(cu_new, "cu_new", i32, (B + 1,), dev), kp, ks, vp, vs, code, cp,
+                                _at(stream, dev)))
 
 
 def ispa_kvq_read(desc: KvqDesc, kvq, block_table, cu_out, k_out, v_out, seq_begin=None, stream=None) -> None:
     """Reads positions seq_begin[b] + i of each sequence back into the packed k_out, v_out [T, H_kv, d]."""
-    s = _Seq()
+    dev, i32 = _device(kvq, "kvq"), _seq()[0]
     B, T = cu_out.shape[0] - 1, k_out.shape[0]
-    shape = (T, desc.H_kv, desc.head_dim)
-    cp, tp = s.cache(desc, kvq, block_table, B)
-    begin = None if seq_begin is None else s.ptr(seq_begin, "seq_begin", s.ints, (B,))
-    _check(lib().ispa_kvq_read(ctypes.byref(desc), B, T, tp, block_table.shape[1], begin,
-                               s.ptr(cu_out, "cu_out", s.ints, (B + 1,)), cp, s.ptr(k_out, "k_out", k_out.dtype, shape),
-                               s.ptr(v_out, "v_out", k_out.dtype, shape), s.code.get(k_out.dtype, -1),
-                               _stream(stream)))
+    shape, dtype = (T, desc.H_kv, desc.head_dim), k_out.dtype
+    cp, tp, wide = _cache(desc, kvq, block_table, B, dev)
+    begin = None if seq_begin is None else _flat(seq_begin, "seq_begin", i32, (B,), dev)
+    _check(lib().ispa_kvq_read(desc, B, T, tp, wide, begin, _flat(cu_out, "cu_out", i32, (B + 1,), dev), cp,
+                               _flat(k_out, "k_out", dtype, shape, dev), _flat(v_out, "v_out", dtype, shape, dev),
+                               _seq()[3].get(dtype, -1), _at(stream, dev)))
 
 
 def ispa_attn_kvq_workspace_bytes(desc: AttnSeqDesc, cache: KvqDesc) -> int:
-    return int(lib().ispa_attn_kvq_workspace_bytes(ctypes.byref(desc), ctypes.byref(cache)))
+    return int(lib().ispa_attn_kvq_workspace_bytes(desc, cache))
 
 
-def _seq_outputs(s, desc, T, o, lse, workspace):
-    out = s.torch.float32 if desc.out_dtype == ISPA_F32 else (
-        s.torch.bfloat16 if desc.out_dtype == ISPA_BF16 else s.torch.float16)
-    op = s.ptr(o, "o", out, (T, desc.H, desc.head_dim))
-    lp = None if lse is None else s.ptr(lse, "lse", s.f32, (T, desc.H))
-    wp = s.ptr(workspace, "workspace", s.bytes_, (None,))
-    return op, lp, wp, workspace.shape[0]
+def _outputs(desc, T, o, lse, workspace, dev):
+    """Addresses of o, lse and the workspace, and the workspace's size."""
+    env = _seq()
+    shape = (T, desc.H, desc.head_dim)
+    if env[3].get(getattr(o, "dtype", None), -1) != desc.out_dtype:
+        raise _explain(o, "o", f"ISPA dtype {desc.out_dtype}", shape, dev)
+    if workspace is None:
+        raise ValueError("workspace: required")
+    n = workspace.numel()
+    return (_flat(o, "o", o.dtype, shape, dev), None if lse is None else _flat(lse, "lse", env[2], shape[:2], dev),
+            _flat(workspace, "workspace", env[1], (n,), dev), n)
 
 
 def ispa_attn_kvq(desc: AttnSeqDesc, cache: KvqDesc, q, kvq, block_table, seq_lens, cu_q, o, lse=None, workspace=None,
                   stream=None) -> None:
     """Attention of the packed queries q [T, H, d] over each sequence's quantised cache."""
-    s = _Seq()
-    qp, T, qs, _ = s.rows(q, "q", desc.H, desc.head_dim, desc.in_dtype)
-    cp, tp = s.cache(cache, kvq, block_table, desc.B)
-    op, lp, wp, wn = _seq_outputs(s, desc, T, o, lse, workspace)
-    _check(lib().ispa_attn_kvq(ctypes.byref(desc), ctypes.byref(cache), T,
-                               s.ptr(cu_q, "cu_q", s.ints, (desc.B + 1,)), tp, block_table.shape[1],
-                               s.ptr(seq_lens, "seq_lens", s.ints, (desc.B,)), qp, qs, cp, op, lp, wp, wn,
-                               _stream(stream)))
+    dev, i32, B = _device(q, "q"), _seq()[0], desc.B
+    qp, T, qs = _rows(q, "q", desc.H, desc.head_dim, desc.in_dtype, dev)
+    cp, tp, wide = _cache(cache, kvq, block_table, B, dev)
+    op, lp, wp, wn = _outputs(desc, T, o, lse, workspace, dev)
+    _check(lib().ispa_attn_kvq(desc, cache, T, _flat(cu_q, "cu_q", i32, (B + 1,), dev), tp, wide,
+                               _flat(seq_lens, "seq_lens", i32, (B,), dev), qp, qs, cp, op, lp, wp, wn,
+                               _at(stream, dev)))
 
 
 def ispa_attn_prompt_workspace_bytes(desc: AttnSeqDesc) -> int:
-    return int(lib().ispa_attn_prompt_workspace_bytes(ctypes.byref(desc)))
+    return int(lib().ispa_attn_prompt_workspace_bytes(desc))
 
 
 def ispa_attn_prompt(desc: AttnSeqDesc, q, k, v, cu_q, cu_k, o, lse=None, workspace=None, stream=None) -> None:
     """Attention of packed prompts: q [Tq, H, d] over k, v [Tk, H_kv, d]."""
-    s = _Seq()
-    qp, Tq, qs, _ = s.rows(q, "q", desc.H, desc.head_dim, desc.in_dtype)
-    kp, Tk, ks, _ = s.rows(k, "k", desc.H_kv, desc.head_dim, desc.in_dtype)
-    vp, Tv, vs, _ = s.rows(v, "v", desc.H_kv, desc.head_dim, desc.in_dtype)
+    dev, i32, B = _device(q, "q"), _seq()[0], desc.B
+    qp, Tq, qs = _rows(q, "q", desc.H, desc.head_dim, desc.in_dtype, dev)
+    kp, Tk, ks = _rows(k, "k", desc.H_kv, desc.head_dim, desc.in_dtype, dev)
+    vp, Tv, vs = _rows(v, "v", desc.H_kv, desc.head_dim, desc.in_dtype, dev)
     if Tk != Tv:
         raise ValueError(f"k has {Tk} rows, v {Tv}")
-    op, lp, wp, wn = _seq_outputs(s, desc, Tq, o, lse, workspace)
-    _check(lib().ispa_attn_prompt(ctypes.byref(desc), Tq, Tk, s.ptr(cu_q, "cu_q", s.ints, (desc.B + 1,)),
-                                  s.ptr(cu_k, "cu_k", s.ints, (desc.B + 1,)), qp, qs, kp, ks, vp, vs, op, lp, wp, wn,
-                                  _stream(stream)))
+    op, lp, wp, wn = _outputs(desc, Tq, o, lse, workspace, dev)
+    _check(lib().ispa_attn_prompt(desc, Tq, Tk, _flat(cu_q, "cu_q", i32, (B + 1,), dev),
+                                  _flat(cu_k, "cu_k", i32, (B + 1,), dev), qp, qs, kp, ks, vp, vs, op, lp, wp, wn,
+                                  _at(stream, dev)))
 
 
 lib()

@@ -25,6 +25,8 @@
 // Channels are assigned to operand positions so that each lane's bytes of a
 // row are contiguous: Q is permuted to match, and O comes out in runs of d/8.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "kvq.cuh"
 #include "seq.cuh"
@@ -33,10 +35,9 @@ namespace ispa {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRows = 16;   // query rows of an item
 constexpr int kTile = 32;   // tokens of a warp's tile
-constexpr int kMinUnit = kWarps;  // tiles a CTA gets at least: one per warp
+constexpr int kMinUnit = 8;       // tiles a CTA gets at least
 constexpr int kMinPart = 4;
 constexpr float kRescale = 8.f;   // the reference maximum moves when passed by more than this (log2)
 constexpr float kNegInf = -INFINITY;
@@ -82,11 +83,16 @@ struct Geo {
   static constexpr int CPR = ROW / 16;  // 16-byte chunks of a row
   static constexpr int CODE = kTile * ROW, SCALE = kTile * REC;
   static constexpr int STAGE = 2 * (CODE + SCALE);
-  static constexpr int STAGES = 3;
+  // As many warps and stages as shared memory holds, two stages at least: the chain of
+  // a tile (scores, maximum, weights, product) has to be hidden by other warps.
+  // (168 registers a thread with 12 warps, 128 with 16: d = 128 needs the former for O's 64.)
+  static constexpr int WARPS = D == 128 ? 12 : 16;
+  static constexpr int STAGES = (220 << 10) / (WARPS * STAGE) < 4 ? (220 << 10) / (WARPS * STAGE) : 4;
+  static constexpr int THREADS = WARPS * 32;
   static constexpr int KS = D / 16;  // k steps of the first product
   static constexpr int NB = D / 8;   // n blocks of the second
-  static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int MERGE = kWarps * kRows * (D + 2) * 4;
+  static constexpr int RING = WARPS * STAGES * STAGE;
+  static constexpr int MERGE = WARPS * kRows * (D + 2) * 4;
   static constexpr int QBYTES = KS * 32 * 16;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + QBYTES + 256;
 
@@ -139,6 +145,11 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -161,16 +172,23 @@ __device__ __forceinline__ void four_codes(uint32_t w, uint32_t &lo, uint32_t &h
     hi = e4m3x2_to_half2(w >> 16);
   }
 }
-// Nibbles s / 4 and s / 4 + 4 of a word (s = 0, 4, 8, 12) as fp16 values n - 8.
-__device__ __forceinline__ uint32_t two_nibbles(uint32_t w, int s) {
-  return hsub2(((w >> s) & 0x000f000fu) | 0x64006400u, 0x64086408u);  // 1024 + n minus 1032
+// Nibble i of both 16-bit halves of a word as fp16 values (n - 8) f, exactly: with the nibble
+// in mantissa bits 4..7 of 1024 the fp16 number is 1024 + 16 n, and (1024 + 16 n) (f / 16) - 72 f
+// is one fused operation whose operands (f has 4 significant bits) and result (7) are fp16 numbers.
+struct Factor {
+  uint32_t sixteenth, minus72;  // pairs f / 16 and -72 f
+  __device__ __forceinline__ explicit Factor(uint32_t f) : sixteenth(hmul2(f, 0x2c002c00u)), minus72(hmul2(f, 0xd480d480u)) {}
+};
+__device__ __forceinline__ uint32_t two_nibbles(uint32_t w, int i, const Factor &f) {
+  const uint32_t at4 = i == 0 ? w << 4 : i == 1 ? w : w >> (4 * (i - 1));
+  return hfma2((at4 & 0x00f000f0u) | 0x64006400u, f.sixteenth, f.minus72);
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -221,8 +239,11 @@ __device__ __forceinline__ float2 two_scales(const unsigned char *rec, int tok) 
 }
 
 template <int FMT, int D, typename T, typename TO>
-__global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
+__global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqParams P) {
   using Ge = Geo<FMT, D>;
+  constexpr int kWarps = Ge::WARPS, kThreads = Ge::THREADS;
+  // fp16 outputs are as fine as fp16 weights: these then enter as a sum of two fp16 numbers
+  constexpr bool kTwoParts = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ SplitRange range;
   __shared__ long long scratch[kWarps + 6];
@@ -316,15 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
       if (lane == 0) q_unscale[r] = P.scale_log2 * ldexpf(1.f, -e);
     }
     __syncthreads();
-    uint32_t qa[Ge::KS][4];
-#pragma unroll
-    for (int ks = 0; ks < Ge::KS; ++ks) {
-      const uint4 v = reinterpret_cast<const uint4 *>(qh)[ks * 32 + lane];
-      qa[ks][0] = v.x;
-      qa[ks][1] = v.y;
-      qa[ks][2] = v.z;
-      qa[ks][3] = v.w;
-    }
+    const uint4 *qf = reinterpret_cast<const uint4 *>(qh) + lane;  // operand of k step ks: qf[32 ks]
     const float un0 = q_unscale[g], un1 = q_unscale[g + 8];
     // keys that rows g and g + 8 may see
     const int past = len - rows.n + 1;
@@ -355,48 +368,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
                           *vr = kr + Ge::SCALE;
       stage = stage + 1 == Ge::STAGES ? 0 : stage + 1;
 
-      // ---- scores: 16 rows x 32 tokens
+      // ---- scores: 16 rows x 32 tokens, times K's scale (the row's factor comes with the exponent)
       float s[4][4];
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
+      for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
-        const int row = nb * 8 + g;
-        if (FMT == ISPA_KVQ_INT4) {
-          constexpr int WORDS = D / 32;  // words of this lane's D / 4 channels
-          uint32_t w[WORDS];
-          if (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(row, t4));
-            w[0] = v.x, w[1] = v.y, w[WORDS - 2] = v.z, w[WORDS - 1] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(kc + row * Ge::ROW + t4 * 8);
-            w[0] = v.x, w[1] = v.y;
+      if (FMT == ISPA_KVQ_INT4) {
+        constexpr int WORDS = D / 32;  // words of this lane's D / 4 channels
+#pragma unroll
+        for (int np = 0; np < 4; np += 2) {
+          uint32_t w[2][WORDS];
+          uint32_t f[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int row = (np + n) * 8 + g;
+            if (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(row, t4));
+              w[n][0] = v.x, w[n][1] = v.y, w[n][WORDS - 2] = v.z, w[n][WORDS - 1] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2 *>(kc + row * Ge::ROW + t4 * 8);
+              w[n][0] = v.x, w[n][1] = v.y;
+            }
+            f[n] = kr[row * 8 + 4 + t4 * (D / 4) / 32];
           }
-          uint32_t f = kr[row * 8 + 4 + t4 * (D / 4) / 32];
-          f = e4m3x2_to_half2(f | f << 8);
+          const Factor fa(e4m3x2_to_half2(f[0] | f[0] << 8)), fb(e4m3x2_to_half2(f[1] | f[1] << 8));
 #pragma unroll
           for (int i = 0; i < WORDS; ++i) {
-            mma16816(s[nb], qa[2 * i], hmul2(two_nibbles(w[i], 0), f), hmul2(two_nibbles(w[i], 4), f));
-            mma16816(s[nb], qa[2 * i + 1], hmul2(two_nibbles(w[i], 8), f), hmul2(two_nibbles(w[i], 12), f));
+            const uint4 q0 = qf[64 * i], q1 = qf[64 * i + 32];
+            mma16816(s[np], q0, two_nibbles(w[0][i], 0, fa), two_nibbles(w[0][i], 1, fa));
+            mma16816(s[np + 1], q0, two_nibbles(w[1][i], 0, fb), two_nibbles(w[1][i], 1, fb));
+            mma16816(s[np], q1, two_nibbles(w[0][i], 2, fa), two_nibbles(w[0][i], 3, fa));
+            mma16816(s[np + 1], q1, two_nibbles(w[1][i], 2, fb), two_nibbles(w[1][i], 3, fb));
           }
-        } else {
+        }
+      } else {
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(row, t4 + 4 * c));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+          for (int nb = 0; nb < 4; ++nb) v[nb] = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(nb * 8 + g, t4 + 4 * c));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 q0 = qf[32 * (4 * c + i)];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
               uint32_t b0, b1;
-              four_codes<FMT>(w[i], b0, b1);
-              mma16816(s[nb], qa[4 * c + i], b0, b1);
+              four_codes<FMT>(i == 0 ? v[nb].x : i == 1 ? v[nb].y : i == 2 ? v[nb].z : v[nb].w, b0, b1);
+              mma16816(s[nb], q0, b0, b1);
             }
           }
         }
+      }
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
         const float2 ksc = two_scales<Ge::REC>(kr, nb * 8 + 2 * t4);
-        s[nb][0] *= ksc.x * un0;
-        s[nb][1] *= ksc.y * un0;
-        s[nb][2] *= ksc.x * un1;
-        s[nb][3] *= ksc.y * un1;
+        s[nb][0] *= ksc.x;
+        s[nb][1] *= ksc.y;
+        s[nb][2] *= ksc.x;
+        s[nb][3] *= ksc.y;
       }
       if (tile * kTile + kTile > lim_all) {
 #pragma unroll
@@ -434,6 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
         vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, o));
       }
+      mx0 *= un0;
+      mx1 *= un1;
       const int et = (int)(__float_as_uint(vmx) >> 23) - 127;  // floor(log2), -127 for zeros
       if (__any_sync(0xffffffffu, mx0 > m0 + kRescale || mx1 > m1 + kRescale || (m0 == kNegInf && mx0 > kNegInf) ||
                                       (m1 == kNegInf && mx1 > kNegInf) || et > ve)) {
@@ -456,17 +488,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
       }
       const float r0 = m0 == kNegInf ? 0.f : m0, r1 = m1 == kNegInf ? 0.f : m1;
       const float vup = __uint_as_float((uint32_t)(min(127 + 6 - ve, 254)) << 23);  // 2^(6 - ve)
-      uint32_t pa[2][4];
+      uint32_t pa[2][4], pl[2][4];
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) {
-        const float p0 = exp2_fast(s[nb][0] - r0), p1 = exp2_fast(s[nb][1] - r0);
-        const float p2 = exp2_fast(s[nb][2] - r1), p3 = exp2_fast(s[nb][3] - r1);
+        const float p0 = exp2_fast(fmaf(s[nb][0], un0, -r0)), p1 = exp2_fast(fmaf(s[nb][1], un0, -r0));
+        const float p2 = exp2_fast(fmaf(s[nb][2], un1, -r1)), p3 = exp2_fast(fmaf(s[nb][3], un1, -r1));
         l0 += p0 + p1;
         l1 += p2 + p3;
         const float va = vsc[nb].x * vup, vb = vsc[nb].y * vup;
-        pa[nb >> 1][(nb & 1) * 2] = pack_half2(p0 * va, p1 * vb);
-        pa[nb >> 1][(nb & 1) * 2 + 1] = pack_half2(p2 * va, p3 * vb);
+        const float w0 = p0 * va, w1 = p1 * vb, w2 = p2 * va, w3 = p3 * vb;
+        const uint32_t h0 = pack_half2(w0, w1), h1 = pack_half2(w2, w3);
+        pa[nb >> 1][(nb & 1) * 2] = h0;
+        pa[nb >> 1][(nb & 1) * 2 + 1] = h1;
+        if (kTwoParts) {
+          const float2 f0 = unpack16(h0, static_cast<const __half *>(nullptr));
+          const float2 f1 = unpack16(h1, static_cast<const __half *>(nullptr));
+          pl[nb >> 1][(nb & 1) * 2] = pack_half2(w0 - f0.x, w1 - f0.y);
+          pl[nb >> 1][(nb & 1) * 2 + 1] = pack_half2(w2 - f1.x, w3 - f1.y);
+        }
       }
+      auto product = [&](float(&c)[4], int kb, uint32_t b0, uint32_t b1) {
+        mma16816(c, make_uint4(pa[kb][0], pa[kb][1], pa[kb][2], pa[kb][3]), b0, b1);
+        if (kTwoParts) mma16816(c, make_uint4(pl[kb][0], pl[kb][1], pl[kb][2], pl[kb][3]), b0, b1);
+      };
 
       // ---- O += P V
 #pragma unroll
@@ -487,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
             }
             f[i] = vr[row * 8 + 4 + g * (D / 8) / 32];
           }
-          const uint32_t fa = e4m3x2_to_half2(f[0] | f[1] << 8), fb = e4m3x2_to_half2(f[2] | f[3] << 8);
+          const Factor fa(e4m3x2_to_half2(f[0] | f[1] << 8)), fb(e4m3x2_to_half2(f[2] | f[3] << 8));
 #pragma unroll
           for (int i = 0; i < WORDS; ++i)
 #pragma unroll
@@ -496,8 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
               const uint32_t xb = prmt(w[2][i], w[3][i], hw ? 0x7632 : 0x5410);
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                mma16816(acc[i * 8 + hw * 4 + c], pa[kb], hmul2(two_nibbles(xa, 4 * c), fa),
-                         hmul2(two_nibbles(xb, 4 * c), fb));
+                product(acc[i * 8 + hw * 4 + c], kb, two_nibbles(xa, c, fa), two_nibbles(xb, c, fb));
             }
         } else {
           constexpr int WORDS = D / 32;
@@ -520,10 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kvq_kernel(KvqParams P) {
             four_codes<FMT>(prmt(w[0][i], w[1][i], 0x7362), a2, a3);
             four_codes<FMT>(prmt(w[2][i], w[3][i], 0x5140), b0, b1);
             four_codes<FMT>(prmt(w[2][i], w[3][i], 0x7362), b2, b3);
-            mma16816(acc[4 * i], pa[kb], a0, b0);
-            mma16816(acc[4 * i + 1], pa[kb], a1, b1);
-            mma16816(acc[4 * i + 2], pa[kb], a2, b2);
-            mma16816(acc[4 * i + 3], pa[kb], a3, b3);
+            product(acc[4 * i], kb, a0, b0);
+            product(acc[4 * i + 1], kb, a1, b1);
+            product(acc[4 * i + 2], kb, a2, b2);
+            product(acc[4 * i + 3], kb, a3, b3);
           }
         }
       }
@@ -651,11 +694,12 @@ template <int FMT, int D, typename T, typename TO>
 ispa_status launch_one(const KvqParams &P, cudaStream_t s) {
   using Ge = Geo<FMT, D>;
   auto kern = attn_kvq_kernel<FMT, D, T, TO>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ge::SMEM);
-  if (e != cudaSuccess) return cuda_status(e, "attn_kvq shared memory");
-  kern<<<P.nc, kThreads, Ge::SMEM, s>>>(P);
+  static std::atomic<void *> prepared{nullptr};
+  ispa_status st = allow_smem(reinterpret_cast<const void *>(kern), Ge::SMEM, prepared, "attn_kvq shared memory");
+  if (st != ISPA_OK) return st;
+  kern<<<P.nc, Ge::THREADS, Ge::SMEM, s>>>(P);
   note_launch();
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e, "attn_kvq launch");
   // the merge is launched ahead of the kernel's end and waits for it on the device
   cudaLaunchAttribute at[1];

@@ -40,6 +40,7 @@
 // 16-key steps that hold a visible key are issued, and the issuing warp zeroes
 // the rows that remain of the last one (0 * Inf would not be 0).
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -776,11 +777,12 @@ ispa_status launch_one(const CUtensorMap &tq, const CUtensorMap &tk, const CUten
   auto kern = attn_prompt_kernel<D, T, TO>;
   constexpr int smem = sizeof(PromptSmem<D>);
   static_assert(smem <= 232448, "shared memory of a block");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_status(e, "attn_prompt shared memory");
+  static std::atomic<void *> prepared{nullptr};
+  ispa_status st = allow_smem(reinterpret_cast<const void *>(kern), smem, prepared, "attn_prompt shared memory");
+  if (st != ISPA_OK) return st;
   kern<<<P.nc, kThreads, smem, s>>>(tq, tk, tv, P);
   note_launch();
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e, "attn_prompt launch");
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ispa.h"
 #include "common.cuh"
 
@@ -117,6 +119,17 @@ ispa_status launch_quant_rows(int M, int K, const void *x, int fmt, void *q, flo
 ispa_status launch_quant_cols(int K, int N, const void *W, int fmt, void *qT, float *scale, cudaStream_t s);
 ispa_status launch_gemm_q8(int M, int N, int K, const void *qa, const float *sa, const void *qT, const float *sw,
                            int fmt, void *y, ispa_dtype ydt, cudaStream_t s);
+
+// Lets a kernel use `bytes` of dynamic shared memory: a property of its context, so it is
+// set again only when the context is not the one that `done` remembers (one per kernel).
+inline ispa_status allow_smem(const void *kernel, int bytes, std::atomic<void *> &done, const char *what) {
+  void *ctx = current_context();
+  if (ctx && done.load(std::memory_order_acquire) == ctx) return ISPA_OK;
+  const ispa_status st =
+      cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), what);
+  if (st == ISPA_OK) done.store(ctx, std::memory_order_release);
+  return st;
+}
 
 // sequences: the quantised paged cache (kvq.cu), attention over it (attn_kvq.cu)
 // and over packed prompts (attn_prompt.cu)
