@@ -1,14 +1,15 @@
 // attn_kvq.cu -- attention of a sequence's newest tokens over its quantised paged cache.
 //
 // For one sequence and one K/V head the query rows are the n new tokens times
-// the group's H / H_kv heads (row = token * group + head), taken 16 at a time:
-// one 16-row operand of the m16n8k16 matrix instruction, so that a decoding
-// step's grouped heads share every byte of the cache.  The work is bound by
-// the cache's bytes; the matrix instructions only have to keep up with them
-// (16 rows x 2 d flop a byte), which the register-fed form does without the
-// 128-row tiles and tensor-memory round trips of the prompt kernel.
+// the group's H / H_kv heads (row = token * group + head), taken 8 or 16 at a
+// time.  The work is bound by the cache's bytes and, close behind, by the
+// instructions that turn codes into operands, so the rows are the narrow side of
+// the matrix instruction (m16n8k16): 16 tokens of K (or 16 channels of V) times
+// 16 channels (tokens) are one operand, 8 rows the other.  Scores are formed as
+// S^T = K Q^T, and O^T = V^T P^T; P^T is S^T transposed in 8 x 8 blocks by
+// movmatrix.
 //
-// A CTA's eight warps work on the same 16 rows and each on every eighth
+// A CTA's warps work on the same rows and each on every 12th or 16th
 // 32-token tile, with a private softmax state and a private ring of tiles in
 // shared memory, filled by asynchronous 16-byte copies straight from the pages
 // (the page of a tile is looked up one tile ahead; tokens past the length are
@@ -35,7 +36,7 @@ namespace ispa {
 
 namespace {
 
-constexpr int kRows = 16;   // query rows of an item
+constexpr int kMaxRows = 16;  // query rows of an item: 8 NR, NR = 1 or 2 blocks of 8
 constexpr int kTile = 32;   // tokens of a warp's tile
 constexpr int kMinUnit = 8;       // tiles a CTA gets at least
 constexpr int kMinPart = 4;
@@ -58,14 +59,14 @@ struct KvqParams {
   int *err;
 };
 
-template <int D>
-constexpr int part_floats() { return kRows * (D + 2); }
+template <int D, int NR>
+constexpr int part_floats() { return 8 * NR * (D + 2); }
 
 // Steps of a sequence: tiles x row blocks x heads.
 struct KvqCost {
   const int *cu, *lens;
-  int T, cap, G, H_kv;
-  __device__ int blocks(int b) const { return (int)(((long long)seq_rows(cu, b, T).n * G + kRows - 1) / kRows); }
+  int T, cap, G, H_kv, rows;  // rows: of a block
+  __device__ int blocks(int b) const { return (int)(((long long)seq_rows(cu, b, T).n * G + rows - 1) / rows); }
   __device__ int tiles(int b) const { return max(1, (seq_len(lens, b, cap) + kTile - 1) / kTile); }
   __device__ long long cost(int b) const { return (long long)blocks(b) * H_kv * tiles(b); }
   __device__ int item(int b, long long off, long long *s, long long *e) const {
@@ -76,24 +77,25 @@ struct KvqCost {
   }
 };
 
-template <int FMT, int D>
+template <int FMT, int D, int NR>
 struct Geo {
   static constexpr int ROW = FMT == ISPA_KVQ_INT4 ? D / 2 : D;
   static constexpr int REC = FMT == ISPA_KVQ_INT4 ? 8 : 4;
   static constexpr int CPR = ROW / 16;  // 16-byte chunks of a row
   static constexpr int CODE = kTile * ROW, SCALE = kTile * REC;
   static constexpr int STAGE = 2 * (CODE + SCALE);
-  // As many warps and stages as shared memory holds, two stages at least: the chain of
-  // a tile (scores, maximum, weights, product) has to be hidden by other warps.
-  // (168 registers a thread with 12 warps, 128 with 16: d = 128 needs the former for O's 64.)
-  static constexpr int WARPS = D == 128 ? 12 : 16;
+  static constexpr int ROWS = 8 * NR;
+  // As many warps and stages as shared memory and registers hold (168 a thread with 12
+  // warps, 128 with 16): the chain of a tile -- scores, maximum, weights, product -- has to
+  // be hidden by other warps.
+  static constexpr int WARPS = STAGE > 8192 || (D == 128 && NR == 2) ? 12 : 16;
   static constexpr int STAGES = (220 << 10) / (WARPS * STAGE) < 4 ? (220 << 10) / (WARPS * STAGE) : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int KS = D / 16;  // k steps of the first product
-  static constexpr int NB = D / 8;   // n blocks of the second
+  static constexpr int MB = D / 16;  // blocks of 16 channels of the second
   static constexpr int RING = WARPS * STAGES * STAGE;
-  static constexpr int MERGE = WARPS * kRows * (D + 2) * 4;
-  static constexpr int QBYTES = KS * 32 * 16;
+  static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;
+  static constexpr int QBYTES = KS * NR * 32 * 8;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + QBYTES + 256;
 
   // Byte offset of a 16-byte chunk of a K row / V row in its tile.  K is read
@@ -128,6 +130,10 @@ struct Geo {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1 + %2], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -168,8 +174,10 @@ __device__ __forceinline__ void four_codes(uint32_t w, uint32_t &lo, uint32_t &h
     lo = hsub2(prmt(w, 0x64646464u, 0x4140), 0x64806480u);
     hi = hsub2(prmt(w, 0x64646464u, 0x4342), 0x64806480u);
   } else {
-    lo = e4m3x2_to_half2(w & 0xffffu);
-    hi = e4m3x2_to_half2(w >> 16);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 // Nibble i of both 16-bit halves of a word as fp16 values (n - 8) f, exactly: with the nibble
@@ -198,50 +206,69 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // One 32-token tile of K and V (codes and scale records) into a ring stage.
+// Tiles that lie wholly below the length take copies with constant offsets from
+// one address a half; the others fill what is missing with zeros.
+template <int FMT, int D, int I>
+__device__ __forceinline__ void copy_rows(uint32_t dst, int half, const unsigned char *ks, const unsigned char *vs,
+                                          int ch, int r0) {
+  using Ge = Geo<FMT, D, 1>;
+  constexpr int RPI = 32 / Ge::CPR;  // rows of one pass of the warp
+  if constexpr (I < 16 / RPI) {
+    cp_async16_at<I * RPI * Ge::ROW>(dst + Ge::k_off(half * 16 + I * RPI + r0, ch), ks);
+    cp_async16_at<I * RPI * Ge::ROW>(dst + Ge::CODE + Ge::v_off(half * 16 + I * RPI + r0, ch), vs);
+    copy_rows<FMT, D, I + 1>(dst, half, ks, vs, ch, r0);
+  }
+}
+
 template <int FMT, int D>
 __device__ __forceinline__ void load_tile(const KvqView &c, uint32_t dst, int h, int tok0, int len, int pg0, int pg1) {
-  using Ge = Geo<FMT, D>;
+  using Ge = Geo<FMT, D, 1>;
   const int lane = threadIdx.x & 31;
   const int mask = (1 << c.page_log2) - 1;
-  constexpr int RPI = 32 / Ge::CPR;  // rows of one pass of the warp
+  constexpr int RPI = 32 / Ge::CPR;
+  constexpr int SC = Ge::REC;  // 16-byte pieces of 16 scale records
   const int ch = lane % Ge::CPR, r0 = lane / Ge::CPR;
+  const bool full = tok0 + kTile <= len && (pg0 | pg1) >= 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int pg = half ? pg1 : pg0, t0 = tok0 + half * 16;
     const long long row0 = c.row(pg < 0 ? 0 : pg, h, t0 & mask);
-    const unsigned char *ks = c.k_code + row0 * Ge::ROW, *vs = c.v_code + row0 * Ge::ROW;
+    const uint32_t rec = dst + 2 * Ge::CODE + (lane < SC ? 0 : Ge::SCALE) + half * 16 * Ge::REC + (lane % SC) * 16;
+    const unsigned char *s = (lane < SC ? c.k_scale : c.v_scale) + row0 * Ge::REC;
+    if (full) {
+      const long long at = row0 * Ge::ROW + lane * 16;
+      copy_rows<FMT, D, 0>(dst, half, c.k_code + at, c.v_code + at, ch, r0);
+      if (lane < 2 * SC) cp_async16(rec, s + (lane % SC) * 16, 16);
+    } else {
+      const unsigned char *ks = c.k_code + row0 * Ge::ROW, *vs = c.v_code + row0 * Ge::ROW;
 #pragma unroll
-    for (int i = 0; i < 16 / RPI; ++i) {
-      const int r = i * RPI + r0;
-      const bool on = pg >= 0 && t0 + r < len;
-      const int off = on ? r * Ge::ROW + ch * 16 : 0;
-      cp_async16(dst + Ge::k_off(half * 16 + r, ch), ks + off, on ? 16 : 0);
-      cp_async16(dst + Ge::CODE + Ge::v_off(half * 16 + r, ch), vs + off, on ? 16 : 0);
-    }
-    // scale records: 16 REC bytes of each half, lanes 0.. of K then of V
-    constexpr int SC = 16 * Ge::REC / 16;
-    if (lane < 2 * SC) {
-      const int i = lane % SC;
-      const int tok = t0 + i * (16 / Ge::REC);
-      const int bytes = pg >= 0 ? min(16, max(0, (len - tok) * Ge::REC)) : 0;
-      const unsigned char *s = (lane < SC ? c.k_scale : c.v_scale) + row0 * Ge::REC + (bytes ? i * 16 : 0);
-      cp_async16(dst + 2 * Ge::CODE + (lane < SC ? 0 : Ge::SCALE) + half * 16 * Ge::REC + i * 16, s, bytes);
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = i * RPI + r0;
+        const bool on = pg >= 0 && t0 + r < len;
+        const int off = on ? r * Ge::ROW + ch * 16 : 0;
+        cp_async16(dst + Ge::k_off(half * 16 + r, ch), ks + off, on ? 16 : 0);
+        cp_async16(dst + Ge::CODE + Ge::v_off(half * 16 + r, ch), vs + off, on ? 16 : 0);
+      }
+      if (lane < 2 * SC) {
+        const int tok = t0 + (lane % SC) * (16 / Ge::REC);
+        const int bytes = pg >= 0 ? min(16, max(0, (len - tok) * Ge::REC)) : 0;
+        cp_async16(rec, s + (bytes ? (lane % SC) * 16 : 0), bytes);
+      }
     }
   }
 }
 
-// fp32 scales of tokens nb * 8 + 2t and + 1 of a tile.
-template <int REC>
-__device__ __forceinline__ float2 two_scales(const unsigned char *rec, int tok) {
-  if (REC == 4) return *reinterpret_cast<const float2 *>(rec + tok * 4);
-  const float4 f = *reinterpret_cast<const float4 *>(rec + tok * 8);
-  return make_float2(f.x, f.z);
+// An 8 x 8 block of 16-bit values, one row of pairs per four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-template <int FMT, int D, typename T, typename TO>
-__global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqParams P) {
-  using Ge = Geo<FMT, D>;
-  constexpr int kWarps = Ge::WARPS, kThreads = Ge::THREADS;
+template <int FMT, int D, int NR, typename T, typename TO>
+__global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, 1) attn_kvq_kernel(KvqParams P) {
+  using Ge = Geo<FMT, D, NR>;
+  constexpr int kWarps = Ge::WARPS, kThreads = Ge::THREADS, kRows = Ge::ROWS;
   // fp16 outputs are as fine as fp16 weights: these then enter as a sum of two fp16 numbers
   constexpr bool kTwoParts = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -251,7 +278,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
   unsigned char *qh = smem + (Ge::RING > Ge::MERGE ? Ge::RING : Ge::MERGE);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const KvqCost cost = {P.cu, P.lens, P.T, P.cap, P.G, P.c.H_kv};
+  const KvqCost cost = {P.cu, P.lens, P.T, P.cap, P.G, P.c.H_kv, kRows};
   if (threadIdx.x < 2) P.meta[2 * blockIdx.x + threadIdx.x].state = 0;
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < P.B; b += kThreads)
@@ -302,7 +329,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
     }
     pages(my0 + (Ge::STAGES - 1) * kWarps, np0, np1);
 
-    // ---- Q: 16 rows as fp16, scaled by a power of two per row, in operand order
+    // ---- Q: the rows as fp16, scaled by a power of two per row, in operand order
     for (int r = warp; r < kRows; r += kWarps) {
       constexpr int PER = D / 32;
       float x[PER];
@@ -331,27 +358,41 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
       for (int i = 0; i < PER; ++i) {
         int ks, t, half, el;
         Ge::q_pos(lane * PER + i, ks, t, half, el);
-        const int reg = half * 2 + (r >> 3);
-        reinterpret_cast<__half *>(qh)[((ks * 32 + (r & 7) * 4 + t) * 4 + reg) * 2 + el] = __float2half_rn(x[i] * up);
+        reinterpret_cast<__half *>(qh)[(((ks * NR + (r >> 3)) * 32 + (r & 7) * 4 + t) * 2 + half) * 2 + el] =
+            __float2half_rn(x[i] * up);
       }
       if (lane == 0) q_unscale[r] = P.scale_log2 * ldexpf(1.f, -e);
     }
     __syncthreads();
-    const uint4 *qf = reinterpret_cast<const uint4 *>(qh) + lane;  // operand of k step ks: qf[32 ks]
-    const float un0 = q_unscale[g], un1 = q_unscale[g + 8];
-    // keys that rows g and g + 8 may see
+    uint2 qb[Ge::KS][NR];
+#pragma unroll
+    for (int ks = 0; ks < Ge::KS; ++ks)
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) qb[ks][nr] = reinterpret_cast<const uint2 *>(qh)[(ks * NR + nr) * 32 + lane];
+    // this lane's rows: 8 nr + 2 t4 + e; the keys that each may see
     const int past = len - rows.n + 1;
-    const int lim0 = P.causal ? min(len, past + (rb * kRows + g) / P.G) : len;
-    const int lim1 = P.causal ? min(len, past + (rb * kRows + g + 8) / P.G) : len;
+    float un[NR][2], m[NR][2], l[NR][2];
+    int lim[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nr * 8 + 2 * t4 + e;
+        un[nr][e] = q_unscale[r];
+        lim[nr][e] = P.causal ? min(len, past + (rb * kRows + r) / P.G) : len;
+        m[nr][e] = kNegInf;
+        l[nr][e] = 0.f;
+      }
     const int lim_all = P.causal ? min(len, past + (rb * kRows) / P.G) : len;  // the first row sees the fewest
 
-    float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
     int ve = -200;  // exponent of the largest V scale so far: weights enter the product times 2^(6 - ve)
-    float acc[Ge::NB][4];
+    float acc[Ge::MB][NR][4];
 #pragma unroll
-    for (int j = 0; j < Ge::NB; ++j)
+    for (int j = 0; j < Ge::MB; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][nr][i] = 0.f;
 
     int stage = 0;
     for (int tile = my0; tile < t_end; tile += kWarps) {
@@ -368,74 +409,84 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
                           *vr = kr + Ge::SCALE;
       stage = stage + 1 == Ge::STAGES ? 0 : stage + 1;
 
-      // ---- scores: 16 rows x 32 tokens, times K's scale (the row's factor comes with the exponent)
-      float s[4][4];
+      // ---- scores of 2 x 16 tokens (lane: tokens g and g + 8 of each) for its rows, times K's scale
+      float s[2][NR][4];
+      float vs[2][2];  // V's scales of the same tokens
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb)
+      for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
-      if (FMT == ISPA_KVQ_INT4) {
-        constexpr int WORDS = D / 32;  // words of this lane's D / 4 channels
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int np = 0; np < 4; np += 2) {
+          for (int i = 0; i < 4; ++i) s[tb][nr][i] = 0.f;
+        const int row0 = tb * 16 + g, row1 = row0 + 8;
+        float ks0, ks1;
+        if (FMT == ISPA_KVQ_INT4) {
+          constexpr int WORDS = D / 32;  // words of this lane's D / 4 channels
           uint32_t w[2][WORDS];
-          uint32_t f[2];
+          const uint2 rec0 = *reinterpret_cast<const uint2 *>(kr + row0 * 8);
+          const uint2 rec1 = *reinterpret_cast<const uint2 *>(kr + row1 * 8);
+          ks0 = __uint_as_float(rec0.x);
+          ks1 = __uint_as_float(rec1.x);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const int row = (np + n) * 8 + g;
             if (D == 128) {
-              const uint4 v = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(row, t4));
+              const uint4 v = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(n ? row1 : row0, t4));
               w[n][0] = v.x, w[n][1] = v.y, w[n][WORDS - 2] = v.z, w[n][WORDS - 1] = v.w;
             } else {
-              const uint2 v = *reinterpret_cast<const uint2 *>(kc + row * Ge::ROW + t4 * 8);
+              const uint2 v = *reinterpret_cast<const uint2 *>(kc + (n ? row1 : row0) * Ge::ROW + t4 * 8);
               w[n][0] = v.x, w[n][1] = v.y;
             }
-            f[n] = kr[row * 8 + 4 + t4 * (D / 4) / 32];
           }
-          const Factor fa(e4m3x2_to_half2(f[0] | f[0] << 8)), fb(e4m3x2_to_half2(f[1] | f[1] << 8));
+          const uint32_t pick = (uint32_t)(t4 * (D / 4) / 32) * 0x11u;  // the factor's byte, twice
+          const Factor f0(e4m3x2_to_half2(prmt(rec0.y, 0u, pick))), f1(e4m3x2_to_half2(prmt(rec1.y, 0u, pick)));
 #pragma unroll
           for (int i = 0; i < WORDS; ++i) {
-            const uint4 q0 = qf[64 * i], q1 = qf[64 * i + 32];
-            mma16816(s[np], q0, two_nibbles(w[0][i], 0, fa), two_nibbles(w[0][i], 1, fa));
-            mma16816(s[np + 1], q0, two_nibbles(w[1][i], 0, fb), two_nibbles(w[1][i], 1, fb));
-            mma16816(s[np], q1, two_nibbles(w[0][i], 2, fa), two_nibbles(w[0][i], 3, fa));
-            mma16816(s[np + 1], q1, two_nibbles(w[1][i], 2, fb), two_nibbles(w[1][i], 3, fb));
+            const uint4 a0 = make_uint4(two_nibbles(w[0][i], 0, f0), two_nibbles(w[1][i], 0, f1),
+                                        two_nibbles(w[0][i], 1, f0), two_nibbles(w[1][i], 1, f1));
+            const uint4 a1 = make_uint4(two_nibbles(w[0][i], 2, f0), two_nibbles(w[1][i], 2, f1),
+                                        two_nibbles(w[0][i], 3, f0), two_nibbles(w[1][i], 3, f1));
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              mma16816(s[tb][nr], a0, qb[2 * i][nr].x, qb[2 * i][nr].y);
+              mma16816(s[tb][nr], a1, qb[2 * i + 1][nr].x, qb[2 * i + 1][nr].y);
+            }
           }
-        }
-      } else {
+        } else {
+          ks0 = *reinterpret_cast<const float *>(kr + row0 * 4);
+          ks1 = *reinterpret_cast<const float *>(kr + row1 * 4);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint4 v[4];
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(row0, t4 + 4 * c));
+            const uint4 v = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(row1, t4 + 4 * c));
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb) v[nb] = *reinterpret_cast<const uint4 *>(kc + Ge::k_off(nb * 8 + g, t4 + 4 * c));
+            for (int i = 0; i < 4; ++i) {
+              uint4 a;
+              four_codes<FMT>(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w, a.x, a.z);
+              four_codes<FMT>(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w, a.y, a.w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 q0 = qf[32 * (4 * c + i)];
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-              uint32_t b0, b1;
-              four_codes<FMT>(i == 0 ? v[nb].x : i == 1 ? v[nb].y : i == 2 ? v[nb].z : v[nb].w, b0, b1);
-              mma16816(s[nb], q0, b0, b1);
+              for (int nr = 0; nr < NR; ++nr) mma16816(s[tb][nr], a, qb[4 * c + i][nr].x, qb[4 * c + i][nr].y);
             }
           }
         }
-      }
+        vs[tb][0] = *reinterpret_cast<const float *>(vr + row0 * Ge::REC);
+        vs[tb][1] = *reinterpret_cast<const float *>(vr + row1 * Ge::REC);
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const float2 ksc = two_scales<Ge::REC>(kr, nb * 8 + 2 * t4);
-        s[nb][0] *= ksc.x;
-        s[nb][1] *= ksc.y;
-        s[nb][2] *= ksc.x;
-        s[nb][3] *= ksc.y;
+        for (int nr = 0; nr < NR; ++nr) {
+          s[tb][nr][0] *= ks0;
+          s[tb][nr][1] *= ks0;
+          s[tb][nr][2] *= ks1;
+          s[tb][nr][3] *= ks1;
+        }
       }
       if (tile * kTile + kTile > lim_all) {
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-          const int tok = tile * kTile + nb * 8 + 2 * t4;
-          if (tok >= lim0) s[nb][0] = kNegInf;
-          if (tok + 1 >= lim0) s[nb][1] = kNegInf;
-          if (tok >= lim1) s[nb][2] = kNegInf;
-          if (tok + 1 >= lim1) s[nb][3] = kNegInf;
+        for (int tb = 0; tb < 2; ++tb) {
+          const int tok = tile * kTile + tb * 16 + g;
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (tok + (i >> 1) * 8 >= lim[nr][i & 1]) s[tb][nr][i] = kNegInf;
         }
       }
       if (bad) {  // tokens whose page does not exist are left out
@@ -444,75 +495,88 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
         pages(tile, p0, p1);
         bad = keep;
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          if ((nb < 2 ? p0 : p1) < 0) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = kNegInf;
+        for (int tb = 0; tb < 2; ++tb)
+          if ((tb ? p1 : p0) < 0) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) s[tb][nr][0] = s[tb][nr][1] = s[tb][nr][2] = s[tb][nr][3] = kNegInf;
+          }
       }
 
-      // ---- running maximum and V scale; O follows when they move
-      float mx0 = kNegInf, mx1 = kNegInf, vmx = 0.f;
-      float2 vsc[4];
+      // ---- the running maximum and V scale move only when some lane's tokens pass them
+      float mx[NR][2];
+      const float vmx = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+      bool move = (int)(__float_as_uint(vmx) >> 23) - 127 > ve;
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        mx0 = fmaxf(mx0, fmaxf(s[nb][0], s[nb][1]));
-        mx1 = fmaxf(mx1, fmaxf(s[nb][2], s[nb][3]));
-        vsc[nb] = two_scales<Ge::REC>(vr, nb * 8 + 2 * t4);
-        vmx = fmaxf(vmx, fmaxf(vsc[nb].x, vsc[nb].y));
-      }
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-        vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, o));
-      }
-      mx0 *= un0;
-      mx1 *= un1;
-      const int et = (int)(__float_as_uint(vmx) >> 23) - 127;  // floor(log2), -127 for zeros
-      if (__any_sync(0xffffffffu, mx0 > m0 + kRescale || mx1 > m1 + kRescale || (m0 == kNegInf && mx0 > kNegInf) ||
-                                      (m1 == kNegInf && mx1 > kNegInf) || et > ve)) {
-        const float n0 = mx0 > m0 ? mx0 : m0, n1 = mx1 > m1 ? mx1 : m1;
-        const float f0 = m0 == kNegInf ? 0.f : exp2_fast(m0 - n0), f1 = m1 == kNegInf ? 0.f : exp2_fast(m1 - n1);
-        const int nv = max(ve, et);
+        for (int e = 0; e < 2; ++e) {
+          mx[nr][e] = fmaxf(fmaxf(s[0][nr][e], s[0][nr][2 + e]), fmaxf(s[1][nr][e], s[1][nr][2 + e])) * un[nr][e];
+          move |= mx[nr][e] > m[nr][e] + kRescale;
+        }
+      if (__any_sync(0xffffffffu, move)) {
+        float v = vmx;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mx[nr][e] = fmaxf(mx[nr][e], __shfl_xor_sync(0xffffffffu, mx[nr][e], o));
+        }
+        const int nv = max(ve, (int)(__float_as_uint(v) >> 23) - 127);  // floor(log2), -127 for zeros
         const float fv = ve == -200 ? 0.f : exp2_fast((float)(ve - nv));
-        m0 = n0;
-        m1 = n1;
         ve = nv;
-        l0 *= f0;
-        l1 *= f1;
 #pragma unroll
-        for (int j = 0; j < Ge::NB; ++j) {
-          acc[j][0] *= f0 * fv;
-          acc[j][1] *= f0 * fv;
-          acc[j][2] *= f1 * fv;
-          acc[j][3] *= f1 * fv;
-        }
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float to = mx[nr][e] > m[nr][e] ? mx[nr][e] : m[nr][e];
+            const float f = m[nr][e] == kNegInf ? 0.f : exp2_fast(m[nr][e] - to);
+            m[nr][e] = to;
+            l[nr][e] *= f;
+#pragma unroll
+            for (int j = 0; j < Ge::MB; ++j) {
+              acc[j][nr][e] *= f * fv;
+              acc[j][nr][2 + e] *= f * fv;
+            }
+          }
       }
-      const float r0 = m0 == kNegInf ? 0.f : m0, r1 = m1 == kNegInf ? 0.f : m1;
+
+      // ---- weights: exp2, times V's scale, to fp16, transposed
       const float vup = __uint_as_float((uint32_t)(min(127 + 6 - ve, 254)) << 23);  // 2^(6 - ve)
-      uint32_t pa[2][4], pl[2][4];
+      uint2 pb[2][NR], pl[2][NR];
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const float p0 = exp2_fast(fmaf(s[nb][0], un0, -r0)), p1 = exp2_fast(fmaf(s[nb][1], un0, -r0));
-        const float p2 = exp2_fast(fmaf(s[nb][2], un1, -r1)), p3 = exp2_fast(fmaf(s[nb][3], un1, -r1));
-        l0 += p0 + p1;
-        l1 += p2 + p3;
-        const float va = vsc[nb].x * vup, vb = vsc[nb].y * vup;
-        const float w0 = p0 * va, w1 = p1 * vb, w2 = p2 * va, w3 = p3 * vb;
-        const uint32_t h0 = pack_half2(w0, w1), h1 = pack_half2(w2, w3);
-        pa[nb >> 1][(nb & 1) * 2] = h0;
-        pa[nb >> 1][(nb & 1) * 2 + 1] = h1;
-        if (kTwoParts) {
-          const float2 f0 = unpack16(h0, static_cast<const __half *>(nullptr));
-          const float2 f1 = unpack16(h1, static_cast<const __half *>(nullptr));
-          pl[nb >> 1][(nb & 1) * 2] = pack_half2(w0 - f0.x, w1 - f0.y);
-          pl[nb >> 1][(nb & 1) * 2 + 1] = pack_half2(w2 - f1.x, w3 - f1.y);
+      for (int tb = 0; tb < 2; ++tb) {
+        const float va = vs[tb][0] * vup, vb = vs[tb][1] * vup;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float ref = m[nr][i & 1] == kNegInf ? 0.f : m[nr][i & 1];
+            const float p = exp2_fast(fmaf(s[tb][nr][i], un[nr][i & 1], -ref));
+            l[nr][i & 1] += p;
+            w[i] = p * (i < 2 ? va : vb);
+          }
+          const uint32_t h0 = pack_half2(w[0], w[1]), h1 = pack_half2(w[2], w[3]);
+          pb[tb][nr] = make_uint2(transpose8(h0), transpose8(h1));
+          if (kTwoParts) {
+            const float2 f0 = unpack16(h0, static_cast<const __half *>(nullptr));
+            const float2 f1 = unpack16(h1, static_cast<const __half *>(nullptr));
+            pl[tb][nr] = make_uint2(transpose8(pack_half2(w[0] - f0.x, w[1] - f0.y)),
+                                    transpose8(pack_half2(w[2] - f1.x, w[3] - f1.y)));
+          }
         }
       }
-      auto product = [&](float(&c)[4], int kb, uint32_t b0, uint32_t b1) {
-        mma16816(c, make_uint4(pa[kb][0], pa[kb][1], pa[kb][2], pa[kb][3]), b0, b1);
-        if (kTwoParts) mma16816(c, make_uint4(pl[kb][0], pl[kb][1], pl[kb][2], pl[kb][3]), b0, b1);
+      auto product = [&](int j, int kb, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          mma16816(acc[j][nr], make_uint4(a0, a1, a2, a3), pb[kb][nr].x, pb[kb][nr].y);
+          if (kTwoParts) mma16816(acc[j][nr], make_uint4(a0, a1, a2, a3), pl[kb][nr].x, pl[kb][nr].y);
+        }
       };
 
-      // ---- O += P V
+      // ---- O^T += V^T P^T
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         const int r = kb * 16 + 2 * t4;
@@ -539,8 +603,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
               const uint32_t xa = prmt(w[0][i], w[1][i], hw ? 0x7632 : 0x5410);
               const uint32_t xb = prmt(w[2][i], w[3][i], hw ? 0x7632 : 0x5410);
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                product(acc[i * 8 + hw * 4 + c], kb, two_nibbles(xa, c, fa), two_nibbles(xb, c, fb));
+              for (int c = 0; c < 4; c += 2)
+                product(i * 4 + hw * 2 + c / 2, kb, two_nibbles(xa, c, fa), two_nibbles(xa, c + 1, fa),
+                        two_nibbles(xb, c, fb), two_nibbles(xb, c + 1, fb));
             }
         } else {
           constexpr int WORDS = D / 32;
@@ -563,10 +628,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
             four_codes<FMT>(prmt(w[0][i], w[1][i], 0x7362), a2, a3);
             four_codes<FMT>(prmt(w[2][i], w[3][i], 0x5140), b0, b1);
             four_codes<FMT>(prmt(w[2][i], w[3][i], 0x7362), b2, b3);
-            product(acc[4 * i], kb, a0, b0);
-            product(acc[4 * i + 1], kb, a1, b1);
-            product(acc[4 * i + 2], kb, a2, b2);
-            product(acc[4 * i + 3], kb, a3, b3);
+            product(2 * i, kb, a0, a1, b0, b1);
+            product(2 * i + 1, kb, a2, a3, b2, b3);
           }
         }
       }
@@ -576,37 +639,36 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
     // ---- merge the warps' states (the rings are idle now)
     cp_wait<0>();
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-    }
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], o);
     __syncthreads();
-    float *mg = reinterpret_cast<float *>(smem);  // [warp][m 16 | l 16 | O 16 x D]
+    float *mg = reinterpret_cast<float *>(smem);  // [warp][m | l | O rows x D]
     {
       float *mine = mg + warp * kRows * (D + 2);
-      if (t4 == 0) {
-        mine[g] = m0;
-        mine[g + 8] = m1;
-        mine[kRows + g] = l0;
-        mine[kRows + g + 8] = l1;
-      }
       const float vdown = ve == -200 ? 0.f : __uint_as_float((uint32_t)(max(127 + ve - 6, 0)) << 23);
-      float *oo = mine + 2 * kRows;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int j = 0; j < Ge::NB; j += 4) {
-          const int ch = (2 * t4 + e) * Ge::NB + j;
-          *reinterpret_cast<float4 *>(oo + g * D + ch) =
-              make_float4(acc[j][e] * vdown, acc[j + 1][e] * vdown, acc[j + 2][e] * vdown, acc[j + 3][e] * vdown);
-          *reinterpret_cast<float4 *>(oo + (g + 8) * D + ch) = make_float4(
-              acc[j][2 + e] * vdown, acc[j + 1][2 + e] * vdown, acc[j + 2][2 + e] * vdown, acc[j + 3][2 + e] * vdown);
+        for (int e = 0; e < 2; ++e) {
+          const int r = nr * 8 + 2 * t4 + e;
+          if (g == 0) {
+            mine[r] = m[nr][e];
+            mine[kRows + r] = l[nr][e];
+          }
+          float4 *oo = reinterpret_cast<float4 *>(mine + 2 * kRows + r * D + g * (D / 8));
+#pragma unroll
+          for (int j = 0; j < Ge::MB; j += 2)
+            oo[j / 2] = make_float4(acc[j][nr][e] * vdown, acc[j][nr][2 + e] * vdown, acc[j + 1][nr][e] * vdown,
+                                    acc[j + 1][nr][2 + e] * vdown);
         }
     }
     __syncthreads();
     const bool whole = t_begin == 0 && t_end == tiles;
     const int slot = 2 * blockIdx.x + (t_begin == 0 ? 1 : 0);
-    float *part = P.part + (size_t)slot * part_floats<D>();
+    float *part = P.part + (size_t)slot * part_floats<D, NR>();
     for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreads) {
       const int r = i / (D / 8), c8 = i % (D / 8) * 8;
       float mm = kNegInf;
@@ -653,8 +715,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::THREADS, 1) attn_kvq_kernel(KvqPa
 }
 
 // Joins the parts of the item that slot 2c + 1 starts (c = blockIdx.x).
-template <int D, typename TO>
+template <int D, int NR, typename TO>
 __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
+  constexpr int kRows = 8 * NR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
   const int n = part_count(P.meta, P.nc, c);
@@ -667,12 +730,12 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   for (int i = threadIdx.x; i < n_rows * (D / 8); i += blockDim.x) {
     const int r = i / (D / 8), c8 = i % (D / 8) * 8;
     float mm = kNegInf;
-    for (int k = 0; k < n; ++k) mm = fmaxf(mm, P.part[(size_t)part_slot(c, k) * part_floats<D>() + r]);
+    for (int k = 0; k < n; ++k) mm = fmaxf(mm, P.part[(size_t)part_slot(c, k) * part_floats<D, NR>() + r]);
     const float ref = mm == kNegInf ? 0.f : mm;
     float ll = 0.f, x[8] = {};
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float *st = P.part + (size_t)part_slot(c, k) * part_floats<D>();
+      const float *st = P.part + (size_t)part_slot(c, k) * part_floats<D, NR>();
       const float f = exp2_fast(st[r] - ref);
       ll += st[kRows + r] * f;
       const float4 a = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8);
@@ -690,10 +753,10 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   }
 }
 
-template <int FMT, int D, typename T, typename TO>
-ispa_status launch_one(const KvqParams &P, cudaStream_t s) {
-  using Ge = Geo<FMT, D>;
-  auto kern = attn_kvq_kernel<FMT, D, T, TO>;
+template <int FMT, int D, int NR, typename T, typename TO>
+ispa_status launch_rows(const KvqParams &P, cudaStream_t s) {
+  using Ge = Geo<FMT, D, NR>;
+  auto kern = attn_kvq_kernel<FMT, D, NR, T, TO>;
   static std::atomic<void *> prepared{nullptr};
   ispa_status st = allow_smem(reinterpret_cast<const void *>(kern), Ge::SMEM, prepared, "attn_kvq shared memory");
   if (st != ISPA_OK) return st;
@@ -711,9 +774,16 @@ ispa_status launch_one(const KvqParams &P, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, TO>, P);
+  e = cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, NR, TO>, P);
   note_launch();
   return cuda_status(e, "kvq_merge launch");
+}
+
+// Row blocks of 8 when a sequence's rows fit one (on the average: the arrays are on the device),
+// else of 16, which read the cache half as often.
+template <int FMT, int D, typename T, typename TO>
+ispa_status launch_one(const KvqParams &P, cudaStream_t s) {
+  return (long long)P.G * P.T <= 8LL * P.B ? launch_rows<FMT, D, 1, T, TO>(P, s) : launch_rows<FMT, D, 2, T, TO>(P, s);
 }
 
 template <int FMT, int D>
@@ -728,7 +798,7 @@ ispa_status launch_typed(const KvqParams &P, ispa_dtype in, ispa_dtype out, cuda
 
 size_t attn_kvq_workspace_bytes(int head_dim) {
   const size_t nc = sm_count();
-  return 2 * nc * (sizeof(PartMeta) + (size_t)kRows * (head_dim + 2) * 4);
+  return 2 * nc * (sizeof(PartMeta) + (size_t)kMaxRows * (head_dim + 2) * 4);
 }
 
 ispa_status launch_attn_kvq(const ispa_attn_seq_desc &d, const ispa_kvq_desc &c, float scale, int T, const int *cu_q,
