@@ -38,8 +38,10 @@ namespace {
 
 constexpr int kMaxRows = 16;  // query rows of an item: 8 NR, NR = 1 or 2 blocks of 8
 constexpr int kTile = 32;   // tokens of a warp's tile
-constexpr int kMinUnit = 8;       // tiles a CTA gets at least
-constexpr int kMinPart = 4;
+constexpr int kMinUnit = 4;       // tiles a CTA gets at least: one per warp
+constexpr int kMaxCtas = 4;       // CTAs per SM at most (Geo::CTAS)
+constexpr int kItem = 8;          // steps counted for an item besides its tiles
+constexpr int kMinPart = kItem + 4;  // steps from an item's start, or to its end, that are not worth cutting off
 constexpr float kRescale = 8.f;   // the reference maximum moves when passed by more than this (log2)
 constexpr float kNegInf = -INFINITY;
 
@@ -68,9 +70,11 @@ struct KvqCost {
   int T, cap, G, H_kv, rows;  // rows: of a block
   __device__ int blocks(int b) const { return (int)(((long long)seq_rows(cu, b, T).n * G + rows - 1) / rows); }
   __device__ int tiles(int b) const { return max(1, (seq_len(lens, b, cap) + kTile - 1) / kTile); }
-  __device__ long long cost(int b) const { return (long long)blocks(b) * H_kv * tiles(b); }
+  // An item costs its tiles and about kItem more: the first tiles' latency, laying out Q, merging the warps.
+  __device__ int steps(int b) const { return tiles(b) + kItem; }
+  __device__ long long cost(int b) const { return (long long)blocks(b) * H_kv * steps(b); }
   __device__ int item(int b, long long off, long long *s, long long *e) const {
-    const int t = tiles(b);
+    const int t = steps(b);
     *s = off / t * t;
     *e = *s + t;
     return 0;
@@ -85,17 +89,19 @@ struct Geo {
   static constexpr int CODE = kTile * ROW, SCALE = kTile * REC;
   static constexpr int STAGE = 2 * (CODE + SCALE);
   static constexpr int ROWS = 8 * NR;
-  // As many warps and stages as shared memory and registers hold (168 a thread with 12
-  // warps, 128 with 16): the chain of a tile -- scores, maximum, weights, product -- has to
-  // be hidden by other warps.
-  static constexpr int WARPS = STAGE > 8192 || (D == 128 && NR == 2) ? 12 : 16;
-  static constexpr int STAGES = (220 << 10) / (WARPS * STAGE) < 4 ? (220 << 10) / (WARPS * STAGE) : 4;
+  // CTAs of four warps, as many to an SM as registers (168 a thread with 12 warps, 128 with
+  // 16) and shared memory hold: while one waits for an item's first tiles or merges its
+  // warps, the others stream.  (One CTA of 12 or 16 warps: see the note at the top.)
+  static constexpr int WARPS = 4;
+  static constexpr int CTAS = STAGE > 8192 || (D == 128 && NR == 2) ? 3 : 4;
+  static constexpr int QBYTES = (D / 16) * NR * 32 * 8;
+  static constexpr int FIT = (233472 / CTAS - 2048 - QBYTES) / (WARPS * STAGE);
+  static constexpr int STAGES = FIT < 4 ? FIT : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int KS = D / 16;  // k steps of the first product
   static constexpr int MB = D / 16;  // blocks of 16 channels of the second
   static constexpr int RING = WARPS * STAGES * STAGE;
   static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;
-  static constexpr int QBYTES = KS * NR * 32 * 8;
   static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + QBYTES + 256;
 
   // Byte offset of a 16-byte chunk of a K row / V row in its tile.  K is read
@@ -266,7 +272,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 template <int FMT, int D, int NR, typename T, typename TO>
-__global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, 1) attn_kvq_kernel(KvqParams P) {
+__global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTAS) attn_kvq_kernel(KvqParams P) {
   using Ge = Geo<FMT, D, NR>;
   constexpr int kWarps = Ge::WARPS, kThreads = Ge::THREADS, kRows = Ge::ROWS;
   // fp16 outputs are as fine as fp16 weights: these then enter as a sum of two fp16 numbers
@@ -294,15 +300,17 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, 1) attn_kvq_kernel(K
   while (left > 0) {
     // ---- the next item of the stretch
     const SeqRows rows = seq_rows(P.cu, b, P.T);
-    const int blocks = cost.blocks(b), tiles = cost.tiles(b);
-    if (off >= (long long)blocks * P.c.H_kv * tiles) {
+    const int blocks = cost.blocks(b), tiles = cost.tiles(b), steps = tiles + kItem;
+    if (off >= (long long)blocks * P.c.H_kv * steps) {
       ++b;
       off = 0;
       continue;
     }
     const int len = seq_len(P.lens, b, P.cap);
-    const int item = (int)(off / tiles), t_begin = (int)(off % tiles);
-    const int t_end = (int)min((long long)tiles, t_begin + left);
+    // step x of an item is its tile x - kItem (a boundary lies at x = 0 or well behind kItem)
+    const int item = (int)(off / steps), x_begin = (int)(off % steps);
+    const int x_end = (int)min((long long)steps, x_begin + left);
+    const int t_begin = max(0, x_begin - kItem), t_end = max(0, x_end - kItem);
     const int h = item / blocks, rb = item % blocks;
     const int n_rows = min(kRows, rows.n * P.G - rb * kRows);
     // ---- this warp's first tiles are on their way while Q is laid out
@@ -709,8 +717,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, 1) attn_kvq_kernel(K
       m->state = t_end == tiles ? 2 : 1;
     }
     __syncthreads();  // the merge area is the next item's ring
-    left -= t_end - t_begin;
-    off += t_end - t_begin;
+    left -= x_end - x_begin;
+    off += x_end - x_begin;
   }
 }
 
@@ -727,22 +735,44 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   const int blocks = (int)(((long long)rows.n * P.G + kRows - 1) / kRows);
   const int h = item / blocks, rb = item % blocks;
   const int n_rows = min(kRows, rows.n * P.G - rb * kRows);
-  for (int i = threadIdx.x; i < n_rows * (D / 8); i += blockDim.x) {
+  // kItems threads take a row's eight columns each; with fewer rows, several threads take
+  // every kSplit-th part of the same columns and are added up in shared memory
+  __shared__ float red[256][9];
+  const int items = n_rows * (D / 8);
+  int split = 1;
+  while (split * 2 * items <= 256 && split < n) split *= 2;
+  for (int i0 = 0; i0 < items; i0 += 256 / split) {
+    const int i = i0 + threadIdx.x / split, sub = threadIdx.x % split;
     const int r = i / (D / 8), c8 = i % (D / 8) * 8;
-    float mm = kNegInf;
-    for (int k = 0; k < n; ++k) mm = fmaxf(mm, P.part[(size_t)part_slot(c, k) * part_floats<D, NR>() + r]);
-    const float ref = mm == kNegInf ? 0.f : mm;
-    float ll = 0.f, x[8] = {};
+    float mm = kNegInf, ll = 0.f, x[8] = {};
+    if (i < items) {
+      for (int k = 0; k < n; ++k) mm = fmaxf(mm, P.part[(size_t)part_slot(c, k) * part_floats<D, NR>() + r]);
+      const float ref = mm == kNegInf ? 0.f : mm;
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float *st = P.part + (size_t)part_slot(c, k) * part_floats<D, NR>();
-      const float f = exp2_fast(st[r] - ref);
-      ll += st[kRows + r] * f;
-      const float4 a = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8);
-      const float4 d = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8 + 4);
-      x[0] += a.x * f, x[1] += a.y * f, x[2] += a.z * f, x[3] += a.w * f;
-      x[4] += d.x * f, x[5] += d.y * f, x[6] += d.z * f, x[7] += d.w * f;
+      for (int k = sub; k < n; k += split) {
+        const float *st = P.part + (size_t)part_slot(c, k) * part_floats<D, NR>();
+        const float f = exp2_fast(st[r] - ref);
+        ll += st[kRows + r] * f;
+        const float4 a = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8);
+        const float4 d = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8 + 4);
+        x[0] += a.x * f, x[1] += a.y * f, x[2] += a.z * f, x[3] += a.w * f;
+        x[4] += d.x * f, x[5] += d.y * f, x[6] += d.z * f, x[7] += d.w * f;
+      }
     }
+    if (split > 1) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) red[threadIdx.x][k] = x[k];
+      red[threadIdx.x][8] = ll;
+      __syncthreads();
+      if (sub == 0)
+        for (int o = 1; o < split; ++o) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] += red[threadIdx.x + o][k];
+          ll += red[threadIdx.x + o][8];
+        }
+      __syncthreads();
+    }
+    if (i >= items || sub != 0) continue;
     const int rr = rb * kRows + r;
     const long long out = (long long)(rows.begin + rr / P.G) * P.H + h * P.G + rr % P.G;
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
@@ -754,8 +784,10 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
 }
 
 template <int FMT, int D, int NR, typename T, typename TO>
-ispa_status launch_rows(const KvqParams &P, cudaStream_t s) {
+ispa_status launch_rows(KvqParams P, cudaStream_t s) {
   using Ge = Geo<FMT, D, NR>;
+  static_assert(Ge::STAGES >= 2 && Ge::CTAS <= kMaxCtas, "ring");
+  P.nc *= Ge::CTAS;
   auto kern = attn_kvq_kernel<FMT, D, NR, T, TO>;
   static std::atomic<void *> prepared{nullptr};
   ispa_status st = allow_smem(reinterpret_cast<const void *>(kern), Ge::SMEM, prepared, "attn_kvq shared memory");
@@ -797,7 +829,7 @@ ispa_status launch_typed(const KvqParams &P, ispa_dtype in, ispa_dtype out, cuda
 }  // namespace
 
 size_t attn_kvq_workspace_bytes(int head_dim) {
-  const size_t nc = sm_count();
+  const size_t nc = (size_t)sm_count() * kMaxCtas;
   return 2 * nc * (sizeof(PartMeta) + (size_t)kMaxRows * (head_dim + 2) * 4);
 }
 
@@ -824,7 +856,7 @@ ispa_status launch_attn_kvq(const ispa_attn_seq_desc &d, const ispa_kvq_desc &c,
   P.o = o;
   P.lse = lse;
   P.meta = static_cast<PartMeta *>(workspace);
-  P.part = reinterpret_cast<float *>(P.meta + 2 * P.nc);
+  P.part = reinterpret_cast<float *>(P.meta + 2 * P.nc * kMaxCtas);
   P.err = e.word;
   const int f = c.fmt * 2 + (c.head_dim == 128 ? 1 : 0);
   switch (f) {
