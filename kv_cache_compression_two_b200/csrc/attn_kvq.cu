@@ -41,7 +41,8 @@ constexpr int kTile = 32;   // tokens of a warp's tile
 constexpr int kMinUnit = 4;       // tiles a CTA gets at least: one per warp
 constexpr int kMaxCtas = 4;       // CTAs per SM at most (Geo::CTAS)
 constexpr int kItem = 8;          // steps counted for an item besides its tiles
-constexpr int kMinPart = kItem + 4;  // steps from an item's start, or to its end, that are not worth cutting off
+constexpr int kMinTail = 4;       // tiles that are worth cutting off
+constexpr int kMinHead = kItem + kMinTail;
 constexpr float kRescale = 8.f;   // the reference maximum moves when passed by more than this (log2)
 constexpr float kNegInf = -INFINITY;
 
@@ -285,11 +286,12 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const KvqCost cost = {P.cu, P.lens, P.T, P.cap, P.G, P.c.H_kv, kRows};
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may take its place on the SMs; it waits for this grid
   if (threadIdx.x < 2) P.meta[2 * blockIdx.x + threadIdx.x].state = 0;
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < P.B; b += kThreads)
       if (seq_rows_bad(P.cu, b, P.T) || __ldg(P.lens + b) != seq_len(P.lens, b, P.cap)) report_seq(P.err, b);
-  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, kMinUnit, kMinPart, &range, scratch);
+  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, kMinUnit, kMinHead, kMinTail, &range, scratch);
 
   long long left = range.x1 - range.x0;
   int b = range.b;
@@ -711,10 +713,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
       }
     }
     if (!whole && threadIdx.x == 0) {
-      PartMeta *m = P.meta + slot;
-      m->b = b;
-      m->item = item;
-      m->state = t_end == tiles ? 2 : 1;
+      PartMeta m = {t_end == tiles ? 2 : 1, rows.begin, rb * kRows, n_rows, h, {}};
+      P.meta[slot] = m;
     }
     __syncthreads();  // the merge area is the next item's ring
     left -= x_end - x_begin;
@@ -728,16 +728,19 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   constexpr int kRows = 8 * NR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
-  const int n = part_count(P.meta, P.nc, c);
+  __shared__ int s_n;
+  if (threadIdx.x < 32) {
+    const int n = part_count(P.meta, P.nc, c);
+    if (threadIdx.x == 0) s_n = n;
+  }
+  __syncthreads();
+  const int n = s_n;
   if (n == 0) return;
-  const int b = P.meta[2 * c + 1].b, item = P.meta[2 * c + 1].item;
-  const SeqRows rows = seq_rows(P.cu, b, P.T);
-  const int blocks = (int)(((long long)rows.n * P.G + kRows - 1) / kRows);
-  const int h = item / blocks, rb = item % blocks;
-  const int n_rows = min(kRows, rows.n * P.G - rb * kRows);
+  const PartMeta own = P.meta[2 * c + 1];
+  const int h = own.head, n_rows = own.count;
   // kItems threads take a row's eight columns each; with fewer rows, several threads take
   // every kSplit-th part of the same columns and are added up in shared memory
-  __shared__ float red[256][9];
+  __shared__ float red[256][11];
   const int items = n_rows * (D / 8);
   int split = 1;
   while (split * 2 * items <= 256 && split < n) split *= 2;
@@ -746,35 +749,41 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
     const int r = i / (D / 8), c8 = i % (D / 8) * 8;
     float mm = kNegInf, ll = 0.f, x[8] = {};
     if (i < items) {
-      for (int k = 0; k < n; ++k) mm = fmaxf(mm, P.part[(size_t)part_slot(c, k) * part_floats<D, NR>() + r]);
-      const float ref = mm == kNegInf ? 0.f : mm;
 #pragma unroll 4
-      for (int k = sub; k < n; k += split) {
+      for (int k = sub; k < n; k += split) {  // (one pass: the loads of several parts are in flight together)
         const float *st = P.part + (size_t)part_slot(c, k) * part_floats<D, NR>();
-        const float f = exp2_fast(st[r] - ref);
-        ll += st[kRows + r] * f;
+        const float mk = st[r], lk = st[kRows + r];
         const float4 a = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8);
         const float4 d = *reinterpret_cast<const float4 *>(st + 2 * kRows + r * D + c8 + 4);
-        x[0] += a.x * f, x[1] += a.y * f, x[2] += a.z * f, x[3] += a.w * f;
-        x[4] += d.x * f, x[5] += d.y * f, x[6] += d.z * f, x[7] += d.w * f;
+        const float to = fmaxf(mm, mk), ref = to == kNegInf ? 0.f : to;
+        const float f0 = exp2_fast(mm - ref), f = exp2_fast(mk - ref);
+        mm = to;
+        ll = ll * f0 + lk * f;
+        x[0] = x[0] * f0 + a.x * f, x[1] = x[1] * f0 + a.y * f, x[2] = x[2] * f0 + a.z * f, x[3] = x[3] * f0 + a.w * f;
+        x[4] = x[4] * f0 + d.x * f, x[5] = x[5] * f0 + d.y * f, x[6] = x[6] * f0 + d.z * f, x[7] = x[7] * f0 + d.w * f;
       }
     }
     if (split > 1) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) red[threadIdx.x][k] = x[k];
       red[threadIdx.x][8] = ll;
+      red[threadIdx.x][9] = mm;
       __syncthreads();
       if (sub == 0)
         for (int o = 1; o < split; ++o) {
+          const float *other = red[threadIdx.x + o];
+          const float to = fmaxf(mm, other[9]), ref = to == kNegInf ? 0.f : to;
+          const float f0 = exp2_fast(mm - ref), f = exp2_fast(other[9] - ref);
+          mm = to;
+          ll = ll * f0 + other[8] * f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] += red[threadIdx.x + o][k];
-          ll += red[threadIdx.x + o][8];
+          for (int k = 0; k < 8; ++k) x[k] = x[k] * f0 + other[k] * f;
         }
       __syncthreads();
     }
     if (i >= items || sub != 0) continue;
-    const int rr = rb * kRows + r;
-    const long long out = (long long)(rows.begin + rr / P.G) * P.H + h * P.G + rr % P.G;
+    const int rr = own.first + r;
+    const long long out = (long long)(own.row + rr / P.G) * P.H + h * P.G + rr % P.G;
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] *= inv;

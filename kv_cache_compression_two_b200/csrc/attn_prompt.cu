@@ -206,9 +206,8 @@ struct PromptWalk {
     g.slot = j == 0 ? 1 : 0;
     g.mode = j == 0 && j1 == total ? 1 : 0;
     if (g.mode == 0) {
-      meta[g.slot].b = b;
-      meta[g.slot].item = h * s.pairs + pair;
-      meta[g.slot].state = j1 == total ? 2 : 1;
+      const PartMeta m = {j1 == total ? 2 : 1, g.q_row, 0, g.n_tok, h, {}};
+      meta[g.slot] = m;
     }
     left -= j1 - j;
     j = j1;
@@ -362,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
+    asm volatile("griddepcontrol.launch_dependents;");  // the merge may take its place on the SMs; it waits for this grid
     P.meta[2 * blockIdx.x].state = 0;
     P.meta[2 * blockIdx.x + 1].state = 0;
   }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = threadIdx.x; b < P.B; b += kThreads)
       if (seq_rows_bad(P.cu_q, b, P.Tq) || seq_rows_bad(P.cu_k, b, P.Tk)) report_error(P.err, ISPA_ERR_INVALID_ARG, b);
   if (warp == 17) tmem_alloc(&sm.tmem_base, 512);
-  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kMinPart, &sm.range, sm.scratch);
+  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kMinPart, kMinPart, &sm.range, sm.scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -736,30 +736,30 @@ __global__ void __launch_bounds__(kTile) prompt_merge_kernel(PromptParams P) {
   const int c = blockIdx.x, w = blockIdx.y, c0 = blockIdx.z * 32, r = threadIdx.x;
   const int n = part_count(P.meta, P.nc, c);
   if (n == 0) return;
-  const PromptCost cost = {P.cu_q, P.cu_k, P.Tq, P.Tk, P.TQ, P.H_kv, P.causal};
-  const int b = P.meta[2 * c + 1].b, item = P.meta[2 * c + 1].item;
-  const PromptSeq s = cost.seq(b);
-  const int h = item / s.pairs, pair = item % s.pairs;
-  const int tok = r / P.G, head = r % P.G, qi = (pair * 2 + w) * P.TQ + tok;
-  if (tok >= P.TQ || qi >= s.n) return;
+  const PartMeta own = P.meta[2 * c + 1];
+  const int tok = r / P.G, head = r % P.G, t = w * P.TQ + tok;
+  if (tok >= P.TQ || t >= own.count) return;
   auto at = [&](int k) { return P.part + ((size_t)part_slot(c, k) * 2 + w) * tile_floats<D>(); };
-  float mm = -INFINITY;
-  for (int k = 0; k < n; ++k) mm = fmaxf(mm, at(k)[r]);
-  const float ref = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f, x[32] = {};
-#pragma unroll 1
+  float mm = -INFINITY, ll = 0.f, x[32] = {};
+#pragma unroll 2
   for (int k = 0; k < n; ++k) {
     const float *p = at(k);
-    const float f = exp2_fast(p[r] - ref);
-    ll += p[kTile + r] * f;
+    const float mk = p[r], lk = p[kTile + r];
     const float4 *po = reinterpret_cast<const float4 *>(p + 2 * kTile) + (c0 / 4) * kTile + r;
+    float4 a[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) a[v] = po[v * kTile];
+    const float to = fmaxf(mm, mk), ref = to == -INFINITY ? 0.f : to;
+    const float f0 = exp2_fast(mm - ref), f = exp2_fast(mk - ref);
+    mm = to;
+    ll = ll * f0 + lk * f;
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const float4 a = po[v * kTile];
-      x[4 * v] += a.x * f, x[4 * v + 1] += a.y * f, x[4 * v + 2] += a.z * f, x[4 * v + 3] += a.w * f;
+      x[4 * v] = x[4 * v] * f0 + a[v].x * f, x[4 * v + 1] = x[4 * v + 1] * f0 + a[v].y * f;
+      x[4 * v + 2] = x[4 * v + 2] * f0 + a[v].z * f, x[4 * v + 3] = x[4 * v + 3] * f0 + a[v].w * f;
     }
   }
-  const long long out = (long long)(s.q0 + qi) * P.H + h * P.G + head;
+  const long long out = (long long)(own.row + t) * P.H + own.head * P.G + head;
   const float inv = ll > 0.f ? 1.f / ll : 0.f;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {

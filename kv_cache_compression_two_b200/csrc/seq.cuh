@@ -9,8 +9,8 @@
 // that a boundary cuts is finished from partial results: each CTA leaves at
 // most two (the end of an item that began before its stretch, slot 2c, and the
 // start of one that goes on behind it, slot 2c + 1), and a second launch
-// merges them.  A boundary that would cut off a part of fewer than min_part
-// steps moves to the item's edge.
+// merges them.  A boundary that would leave fewer than min_head steps before it
+// or fewer than min_tail behind it in its item moves to the item's edge.
 #pragma once
 
 #include "common.cuh"
@@ -74,7 +74,7 @@ struct SplitRange {
 // At most ceil(total / min_unit) CTAs get work.  Called by all NT threads; sw:
 // NT / 32 + 6 values of scratch.
 template <int NT, class F>
-__device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int min_part, SplitRange *r,
+__device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int min_head, int min_tail, SplitRange *r,
                             long long *sw) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (B + NT - 1) / NT;
@@ -130,8 +130,8 @@ __device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int 
     const int b = (int)found[3 * warp];
     long long off = found[3 * warp + 1], s, e;
     const int tag = f.item(b, off, &s, &e);
-    if (off - s < min_part) off = s;
-    else if (e - off < min_part) off = e;
+    if (off - s < min_head) off = s;
+    else if (e - off < min_tail) off = e;
     if (lane == 0) {
       if (warp == 0) {
         r->b = b;
@@ -147,25 +147,33 @@ __device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int 
   __syncthreads();
 }
 
-// What a CTA records of its two partial results (slots 2c and 2c + 1).
-struct PartMeta {
+// What a CTA records of its two partial results (slots 2c and 2c + 1), and of the
+// item that slot 2c + 1 starts: all that the merge needs, in one load.
+struct __align__(16) PartMeta {
   int state;  // 0: none, 1: the item goes on in the next CTA, 2: the item ends here
-  int b, item, spare;
+  int row;    // packed row of the sequence's (tile's) first token
+  int first, count;  // the item's rows: their first (from `row`, in token * group + head), their number
+  int head;   // K/V head
+  int spare[3];
 };
 
 // A stretch's first CTA owns an item that slot 2c + 1 starts; its parts are
 // that slot and slots 2c' of the CTAs behind it up to the first with state 2.
 // Returns their number (0: nothing to merge); part i > 0 is in slot 2 (c + i).
-__device__ __forceinline__ int part_count(const volatile PartMeta *meta, int nc, int c) {
-  if (meta[2 * c + 1].state == 0) return 0;
-  int n = 1;
-  while (c + n < nc) {
-    const int st = meta[2 * (c + n)].state;
-    if (st == 0) break;
-    ++n;
-    if (st == 2) break;
+// Called by a whole warp: 32 states are read at a time.
+__device__ __forceinline__ int part_count(const PartMeta *meta, int nc, int c) {
+  if (*const_cast<const volatile int *>(&meta[2 * c + 1].state) == 0) return 0;
+  const int lane = threadIdx.x & 31;
+  for (int n = 1; c + n < nc; n += 32) {
+    const int at = c + n + lane;
+    const int st = at < nc ? *const_cast<const volatile int *>(&meta[2 * at].state) : 2;
+    const unsigned stop = __ballot_sync(0xffffffffu, st != 1);
+    if (stop) {
+      const int k = __ffs(stop) - 1;
+      return n + k + (__shfl_sync(0xffffffffu, at < nc ? st : 0, k) == 2 ? 1 : 0);
+    }
   }
-  return n;
+  return nc - c;
 }
 
 __device__ __forceinline__ int part_slot(int c, int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); }
