@@ -2,17 +2,20 @@
 //
 // Both are one pass over their bytes and bound by memory (and, for a decoding
 // step's few rows, by the launch).  A row (one token of one head) is handled
-// by d / 8 lanes, 16 bytes of 16-bit values each; a warp takes one token and
-// up to kHeads heads of K and of V, whose loads are all issued before the
+// by d / 16 lanes, 16 values each: with 8 a lane the reductions and reciprocals of
+// a row cost as much as its values.  A warp takes one token
+// and up to kHeads heads of K and of V, whose loads are all issued before the
 // first is used.
 //
-// The codes are decided by quotients with exact operands: 127 x, 448 x and
-// 3136 x / 4096 fit fp32 for 16-bit x, as does amax * g, and the powers of two
-// that keep the quotient in range are exact too.  The quotient of two such
-// numbers is either on a border between two codes or further from it than
-// half an fp32 step (numerator and denominator have at most 18 and 15
-// significant bits, the border 8), so one correctly rounded division gives the
-// code of real arithmetic, ties included.
+// The codes are those of real arithmetic, ties included, without a division an
+// element.  A quotient a / b lies on a border t between two codes or on one side
+// of it; with an approximate reciprocal it is first found to about 2^-22, rounded
+// to the grid that holds the borders (halves for the integer codes, 5 significant
+// bits for e4m3) as t, and then taken as t + (a - t b) / b: a - t b is exact in one
+// fused operation (a = x times 127/128, 49/64 or 7/8 has at most 18 significant
+// bits, b = amax times a 4-bit factor 15, t 9, and the difference is small), so the
+// correction has the right sign, is zero exactly on the border, and otherwise at
+// least 2^-20 of t, which the last addition keeps.
 #include "kvq.cuh"
 #include "seq.cuh"
 
@@ -44,59 +47,86 @@ __device__ __forceinline__ float2 e4m3x2_to_float(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Eight values of a row of W lanes: codes (8 or 4 bytes) and the row's scale record.
+// 1 / b to about 2^-23, for b in [2^-120, 2^121].
+__device__ __forceinline__ float reciprocal(float b) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+  return r;
+}
+
+// a / b to fp32, exactly on, or on the right side of, every multiple of 1 / 2 (|a / b| < 2^21).
+__device__ __forceinline__ float exact_half(float a, float b, float inv) {
+  const float t = __fadd_rn(fmaf(a, inv, 6291456.f), -6291456.f);  // 1.5 * 2^22: rounds to halves
+  return fmaf(fmaf(-t, b, a), inv, t);
+}
+// The same for every number of 5 significant bits: the borders of e4m3.
+__device__ __forceinline__ float exact_e4m3(float a, float b, float inv) {
+  const float t = __uint_as_float((__float_as_uint(a * inv) + 0x40000u) & 0xfff80000u);
+  return copysignf(fmaf(fmaf(-t, b, a), inv, t), a);  // (the sign of zero is kept)
+}
+
+// Sixteen values of a row of W lanes: codes (16 or 8 bytes) and the row's scale record.
 template <int FMT, int W>
-__device__ __forceinline__ void quantise8(const float (&x)[8], uint2 &code, uint2 &rec) {
+__device__ __forceinline__ void quantise16(const float (&x)[16], uint4 &code, uint2 &rec) {
   float am = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
+  for (int i = 0; i < 16; ++i) am = fmaxf(am, fabsf(x[i]));
   float group = am;
 #pragma unroll
   for (int o = 1; o < W; o <<= 1) {
-    if (o == 4) group = am;  // the four lanes of 32 channels
     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    if (o == 1) group = am;  // the two lanes of 32 channels
   }
   const bool some = am >= kLeast;
   const float div = some ? am : 1.f;
   if (FMT == ISPA_KVQ_INT4) {
-    const uint32_t g8 = some ? e4m3x2(group * 0.875f / div * 512.f, 0.f) & 0xffu : 0u;
-    const float step = div * (e4m3x2_to_float(g8).x * (1.f / 512.f));
+    const float gb = div * (1.f / 512.f), ga = group * 0.875f;  // 448 group / amax = ga / gb
+    const float ginv = reciprocal(gb);
+    const uint32_t g8 = some ? e4m3x2(exact_e4m3(ga, gb, ginv), 0.f) & 0xffu : 0u;
     const bool on = g8 != 0;
-    const float over = on ? step : 1.f;
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = fminf(fmaxf(rintf(x[i] * (49.f / 64.f) / over * 8.f), -7.f), 7.f);
-      c |= (uint32_t)((on ? (int)n : 0) + 8) << (4 * i);
-    }
-    code = make_uint2(c, 0u);
-    // the factors of the row's groups, gathered from the first lane of each
-    uint32_t factors = 0;
-#pragma unroll
-    for (int g = 0; g < W / 4; ++g) factors |= __shfl_sync(0xffffffffu, g8, g * 4, W) << (8 * g);
-    rec = make_uint2(__float_as_uint(some ? am / 3136.f : 0.f), factors);
-  } else if (FMT == ISPA_KVQ_INT8) {
+    const float b = on ? gb * e4m3x2_to_float(g8).x * 0.125f : 1.f;  // 3136 x / (amax g) = (49 / 64 x) / b
+    const float inv = reciprocal(b);
     uint32_t c[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = fminf(fmaxf(rintf(x[i] * (127.f / 128.f) / div * 128.f), -127.f), 127.f);
-      c[i >> 2] |= ((uint32_t)(some ? (int)n : 0) & 0xffu) << (8 * (i & 3));
+    for (int i = 0; i < 16; ++i) {
+      const float n = fminf(fmaxf(exact_half(x[i] * (49.f / 64.f), b, inv), -7.f), 7.f);
+      // + 8, rounded to the nearest even integer by the addition of 1.5 * 2^23
+      c[i >> 3] |= (on ? __float_as_uint(n + 12582920.f) & 15u : 8u) << (4 * (i & 7));
     }
-    code = make_uint2(c[0], c[1]);
+    code = make_uint4(c[0], c[1], 0u, 0u);
+    // the factors of the row's groups (two lanes hold each)
+    uint32_t factors = g8 << (8 * ((threadIdx.x & (W - 1)) >> 1));
+#pragma unroll
+    for (int o = 2; o < W; o <<= 1) factors |= __shfl_xor_sync(0xffffffffu, factors, o);
+    rec = make_uint2(__float_as_uint(some ? am / 3136.f : 0.f), factors);
+  } else if (FMT == ISPA_KVQ_INT8) {
+    const float b = div * (1.f / 128.f), inv = reciprocal(b);  // 127 x / amax = (127 / 128 x) / b, at most 127
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t n[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        n[i] = __float_as_uint(exact_half(x[4 * q + i] * (127.f / 128.f), b, inv) + 12582912.f);
+      w[q] = some ? __byte_perm(__byte_perm(n[0], n[1], 0x40), __byte_perm(n[2], n[3], 0x40), 0x5410) : 0u;
+    }
+    code = make_uint4(w[0], w[1], w[2], w[3]);
     rec = make_uint2(__float_as_uint(some ? am / 127.f : 0.f), 0u);
   } else {
-    float y[8];
+    const float b = div * (1.f / 512.f), inv = reciprocal(b);
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = some ? x[i] * 0.875f / div * 512.f : 0.f;
-    code = make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16, e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
+    for (int i = 0; i < 8; ++i)
+      w[i] = some ? e4m3x2(exact_e4m3(x[2 * i] * 0.875f, b, inv), exact_e4m3(x[2 * i + 1] * 0.875f, b, inv)) : 0u;
+    code = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     rec = make_uint2(__float_as_uint(some ? am / 448.f : 0.f), 0u);
   }
 }
 
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads) kvq_write_kernel(RowParams P) {
-  constexpr int W = D / 8;                        // lanes of a row
-  constexpr int kRows = 32 / W;                   // rows of a pass: K and V, and two heads each for d = 64
+  constexpr int W = D / 16;                       // lanes of a row
+  constexpr int kRows = 32 / W;                   // rows of a pass: K and V of kStep heads
   constexpr int kHeads = 4, kStep = kRows / 2;    // heads of a warp, heads of a pass
   constexpr int ROW = FMT == ISPA_KVQ_INT4 ? D / 2 : D, REC = FMT == ISPA_KVQ_INT4 ? 8 : 4;
   const int lane = threadIdx.x & 31;
@@ -108,12 +138,14 @@ __global__ void __launch_bounds__(kThreads) kvq_write_kernel(RowParams P) {
   if (b < 0) return;
   const int sub = lane / W, l = lane % W;
   const bool is_v = sub >= kStep;
-  const T *src = static_cast<const T *>(is_v ? P.v : P.k) + (long long)t * (is_v ? P.vs : P.ks) + l * 8;
-  uint4 in[kHeads / kStep];
+  const T *src = static_cast<const T *>(is_v ? P.v : P.k) + (long long)t * (is_v ? P.vs : P.ks) + l * 16;
+  uint4 in[kHeads / kStep][2];
 #pragma unroll
   for (int i = 0; i < kHeads / kStep; ++i) {
     const int h = h0 + i * kStep + sub % kStep;
-    in[i] = h < P.H_kv ? __ldg(reinterpret_cast<const uint4 *>(src + (long long)h * D)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      in[i][k] = h < P.H_kv ? __ldg(reinterpret_cast<const uint4 *>(src + (long long)h * D) + k) : make_uint4(0, 0, 0, 0);
   }
   const int c0 = __ldg(P.cu + b), c1 = __ldg(P.cu + b + 1);
   const long long pos = (long long)__ldg(P.lens + b) - (c1 - c0) + (t - c0);
@@ -127,23 +159,24 @@ __global__ void __launch_bounds__(kThreads) kvq_write_kernel(RowParams P) {
 #pragma unroll
   for (int i = 0; i < kHeads / kStep; ++i) {
     const int h = h0 + i * kStep + sub % kStep;
-    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-    float x[8];
+    const uint32_t w[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w, in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+    float x[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const float2 f = unpack16(w[j], static_cast<const T *>(nullptr));
       x[2 * j] = f.x;
       x[2 * j + 1] = f.y;
     }
-    uint2 code, rec;
-    quantise8<FMT, W>(x, code, rec);
+    uint4 code;
+    uint2 rec;
+    quantise16<FMT, W>(x, code, rec);
     if (h >= P.H_kv) continue;
     const long long row = P.c.row(page, h, place);
     if (FMT == ISPA_KVQ_INT4) {
-      *reinterpret_cast<uint32_t *>(codes + row * ROW + l * 4) = code.x;
+      *reinterpret_cast<uint2 *>(codes + row * ROW + l * 8) = make_uint2(code.x, code.y);
       if (l == 0) *reinterpret_cast<uint2 *>(scales + row * REC) = rec;
     } else {
-      *reinterpret_cast<uint2 *>(codes + row * ROW + l * 8) = code;
+      *reinterpret_cast<uint4 *>(codes + row * ROW + l * 16) = code;
       if (l == 0) *reinterpret_cast<uint32_t *>(scales + row * REC) = rec.x;
     }
   }
@@ -156,72 +189,85 @@ __device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) { return 
 template <>
 __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
 
+// A warp reads one token of up to four heads (two or four tokens measured the same or worse).  Eight
+// values a lane here, so that a warp's stores are whole lines (sixteen: 43 us instead of 37 for
+// 23400 tokens of 12 heads in int4).
+constexpr int kTokens = 1;
+
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads) kvq_read_kernel(RowParams P) {
   constexpr int W = D / 8;
   constexpr int kRows = 32 / W;
-  constexpr int kHeads = 4, kStep = kRows / 2;
+  constexpr int kHeads = 4, kStep = kRows / 2, kN = kHeads / kStep;
   constexpr int ROW = FMT == ISPA_KVQ_INT4 ? D / 2 : D, REC = FMT == ISPA_KVQ_INT4 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const int h_parts = (P.H_kv + kHeads - 1) / kHeads;
   const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int t = (int)(item / h_parts), h0 = (int)(item % h_parts) * kHeads;
-  if (t >= P.T) return;
-  const int b = seq_of_row(P.cu, P.B, t);
-  if (b < 0) return;
-  const long long pos = (long long)(P.begin ? __ldg(P.begin + b) : 0) + (t - __ldg(P.cu + b));
-  const int page = P.c.page(b, pos);
-  if ((page < 0 || seq_rows_bad(P.cu, b, P.T)) && lane == 0) report_seq(P.err, b);
-  const int place = (int)(pos & ((1 << P.c.page_log2) - 1));
+  const long long t0 = item / h_parts * kTokens;
+  const int h0 = (int)(item % h_parts) * kHeads;
   const int sub = lane / W, l = lane % W;
   const bool is_v = sub >= kStep;
   const unsigned char *codes = is_v ? P.c.v_code : P.c.k_code, *scales = is_v ? P.c.v_scale : P.c.k_scale;
-  uint2 code[kHeads / kStep], rec[kHeads / kStep];
+  uint2 code[kTokens][kN], rec[kTokens][kN];
+  int page[kTokens], seq[kTokens];
 #pragma unroll
-  for (int i = 0; i < kHeads / kStep; ++i) {
-    const int h = h0 + i * kStep + sub % kStep;
-    code[i] = make_uint2(0u, 0u);
-    rec[i] = make_uint2(0u, 0u);
-    if (h >= P.H_kv || page < 0) continue;
-    const long long row = P.c.row(page, h, place);
-    if (FMT == ISPA_KVQ_INT4) {
-      code[i].x = __ldg(reinterpret_cast<const uint32_t *>(codes + row * ROW + l * 4));
-      rec[i] = __ldg(reinterpret_cast<const uint2 *>(scales + row * REC));
-    } else {
-      code[i] = __ldg(reinterpret_cast<const uint2 *>(codes + row * ROW + l * 8));
-      rec[i].x = __ldg(reinterpret_cast<const uint32_t *>(scales + row * REC));
+  for (int k = 0; k < kTokens; ++k) {
+    const int t = (int)(t0 + k);
+    const int b = t0 + k < P.T ? seq_of_row(P.cu, P.B, t) : -1;
+    seq[k] = b;
+    page[k] = -1;
+    if (b < 0) continue;
+    const long long pos = (long long)(P.begin ? __ldg(P.begin + b) : 0) + (t - __ldg(P.cu + b));
+    page[k] = P.c.page(b, pos);
+    if ((page[k] < 0 || seq_rows_bad(P.cu, b, P.T)) && lane == 0) report_seq(P.err, b);
+    const int place = (int)(pos & ((1 << P.c.page_log2) - 1));
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int h = h0 + i * kStep + sub % kStep;
+      code[k][i] = make_uint2(0u, 0u);
+      rec[k][i] = make_uint2(0u, 0u);
+      if (h >= P.H_kv || page[k] < 0) continue;
+      const long long row = P.c.row(page[k], h, place);
+      if (FMT == ISPA_KVQ_INT4) {
+        code[k][i].x = __ldg(reinterpret_cast<const uint32_t *>(codes + row * ROW + l * 4));
+        rec[k][i] = __ldg(reinterpret_cast<const uint2 *>(scales + row * REC));
+      } else {
+        code[k][i] = __ldg(reinterpret_cast<const uint2 *>(codes + row * ROW + l * 8));
+        rec[k][i].x = __ldg(reinterpret_cast<const uint32_t *>(scales + row * REC));
+      }
     }
   }
-  T *dst = static_cast<T *>(is_v ? P.vo : P.ko) + (long long)t * P.H_kv * D + l * 8;
 #pragma unroll
-  for (int i = 0; i < kHeads / kStep; ++i) {
-    const int h = h0 + i * kStep + sub % kStep;
-    if (h >= P.H_kv) continue;
-    const float s = __uint_as_float(rec[i].x);
-    float x[8];
-    if (FMT == ISPA_KVQ_INT4) {
-      const float sg = s * e4m3x2_to_float((rec[i].y >> (8 * (l >> 2))) & 0xffu).x;
+  for (int k = 0; k < kTokens; ++k) {
+    if (seq[k] < 0) continue;
+    T *dst = static_cast<T *>(is_v ? P.vo : P.ko) + (t0 + k) * P.H_kv * D + l * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = (float)((int)((code[i].x >> (4 * j)) & 15u) - 8) * sg;
-      if (page < 0) {
+    for (int i = 0; i < kN; ++i) {
+      const int h = h0 + i * kStep + sub % kStep;
+      if (h >= P.H_kv) continue;
+      const float s = __uint_as_float(rec[k][i].x);
+      const uint32_t w[2] = {code[k][i].x, code[k][i].y};
+      float x[8];
+      if (FMT == ISPA_KVQ_INT4) {
+        const float sg = s * e4m3x2_to_float((rec[k][i].y >> (8 * (l >> 2))) & 0xffu).x;
+        // 1.5 * 2^23 + n has n in its last bits: the conversion is one subtraction
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        for (int j = 0; j < 8; ++j) x[j] = (__uint_as_float(0x4b400000u | ((w[0] >> (4 * j)) & 15u)) - 12582920.f) * sg;
+      } else if (FMT == ISPA_KVQ_INT8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (float)(int)(signed char)((w[j >> 2] >> (8 * (j & 3))) & 0xffu) * s;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = e4m3x2_to_float((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+          x[2 * j] = f.x * s;
+          x[2 * j + 1] = f.y * s;
+        }
       }
-    } else if (FMT == ISPA_KVQ_INT8) {
-      const uint32_t w[2] = {code[i].x, code[i].y};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = (float)(int)(signed char)((w[j >> 2] >> (8 * (j & 3))) & 0xffu) * s;
-    } else {
-      const uint32_t w[2] = {code[i].x, code[i].y};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = e4m3x2_to_float((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-        x[2 * j] = f.x * s;
-        x[2 * j + 1] = f.y * s;
-      }
+      *reinterpret_cast<uint4 *>(dst + (long long)h * D) =
+          page[k] < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                      : make_uint4(pack16<T>(x[0], x[1]), pack16<T>(x[2], x[3]), pack16<T>(x[4], x[5]), pack16<T>(x[6], x[7]));
     }
-    *reinterpret_cast<uint4 *>(dst + (long long)h * D) =
-        make_uint4(pack16<T>(x[0], x[1]), pack16<T>(x[2], x[3]), pack16<T>(x[4], x[5]), pack16<T>(x[6], x[7]));
   }
 }
 
@@ -254,7 +300,8 @@ ispa_status launch_kvq(const ispa_kvq_desc &d, RowParams P, bool write, ispa_dty
   ispa_status st = device_err(&e);
   if (st != ISPA_OK) return st;
   P.err = e.word;
-  const long long items = (long long)P.T * ((d.H_kv + 3) / 4);
+  const long long tokens = write ? P.T : ((long long)P.T + kTokens - 1) / kTokens;
+  const long long items = tokens * ((d.H_kv + 3) / 4);
   const unsigned grid = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
   if (d.fmt == ISPA_KVQ_E4M3)
     launch_rows_fmt<ISPA_KVQ_E4M3>(P, write, d.head_dim, dt, grid, s);
