@@ -53,7 +53,8 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kTile = 128;
 constexpr int kBox = 128 * 128;  // bytes of 128 rows x 64 columns
-constexpr int kMinPart = 4;
+constexpr int kItem = 2;         // steps counted for an item besides its own: filling the pipeline, the output
+constexpr int kMinPart = 4;      // steps that are worth cutting off
 constexpr int kSegs = 4;         // items handed on ahead
 constexpr int kSegReaders = 18;  // producer, issuer, sixteen softmax warps
 constexpr float kThreshold = 8.0f;  // the reference maximum moves when passed by more than this (log2)
@@ -62,6 +63,7 @@ constexpr uint32_t kColS = 0, kColO = 256;
 struct PromptParams {
   int B, H, H_kv, G, TQ;  // G = H / H_kv heads per K/V head, TQ = 128 / G tokens per tile
   int Tq, Tk, causal, nc;
+  int wide;  // o is 32-byte aligned
   float scale_log2;
   const int *cu_q, *cu_k;
   void *o;
@@ -111,11 +113,15 @@ struct PromptCost {
   }
   // keys that the queries below token index t of the sequence see at most
   __device__ int limit(const PromptSeq &s, int t) const { return causal ? s.past + min(t, s.n) : s.len; }
+  // steps of a pair: kItem and its KV tiles
   __device__ int steps(const PromptSeq &s, int pair) const {
-    return max(1, (limit(s, (pair + 1) * 2 * TQ) + kTile - 1) >> 7);
+    return kItem + max(1, (limit(s, (pair + 1) * 2 * TQ) + kTile - 1) >> 7);
   }
   // steps of the pairs before `pair` (< s.pairs), all of them full
   __device__ long long before(const PromptSeq &s, int pair) const {
+    return (long long)kItem * pair + tiles_before(s, pair);
+  }
+  __device__ long long tiles_before(const PromptSeq &s, int pair) const {
     if (!causal) return (long long)pair * max(1, (s.len + kTile - 1) >> 7);
     const int R = 2 * TQ;
     const int ones = min(pair, s.past >= kTile ? 0 : (kTile - s.past) / R);  // pairs of one step
@@ -189,7 +195,9 @@ struct PromptWalk {
       }
       total = c.steps(s, pair);
     }
-    const int j1 = (int)min((long long)total, j + left);
+    // step x of an item is its tile x - kItem (a boundary lies at x = 0 or well behind kItem)
+    const int x1 = (int)min((long long)total, j + left);
+    const int j0 = max(0, j - kItem), j1 = max(0, x1 - kItem);
     const int t0 = pair * 2 * c.TQ;
     g.h = h;
     g.q_row = s.q0 + t0;
@@ -197,20 +205,20 @@ struct PromptWalk {
     g.k_row = s.k0;
     g.len = s.len;
     g.lim = c.causal ? s.past + t0 + 1 : s.len;
-    g.j0 = j;
+    g.j0 = j0;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int lim = g.n_tok > w * c.TQ ? c.limit(s, t0 + (w + 1) * c.TQ) : 0;
-      g.end[w] = max(j, min(j1, (lim + kTile - 1) >> 7));
+      g.end[w] = max(j0, min(j1, (lim + kTile - 1) >> 7));
     }
     g.slot = j == 0 ? 1 : 0;
-    g.mode = j == 0 && j1 == total ? 1 : 0;
+    g.mode = j == 0 && x1 == total ? 1 : 0;
     if (g.mode == 0) {
-      const PartMeta m = {j1 == total ? 2 : 1, g.q_row, 0, g.n_tok, h, {}};
+      const PartMeta m = {x1 == total ? 2 : 1, g.q_row, 0, g.n_tok, h, {}};
       meta[g.slot] = m;
     }
-    left -= j1 - j;
-    j = j1;
+    left -= x1 - j;
+    j = x1;
     return true;
   }
 };
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = threadIdx.x; b < P.B; b += kThreads)
       if (seq_rows_bad(P.cu_q, b, P.Tq) || seq_rows_bad(P.cu_k, b, P.Tk)) report_error(P.err, ISPA_ERR_INVALID_ARG, b);
   if (warp == 17) tmem_alloc(&sm.tmem_base, 512);
-  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kMinPart, kMinPart, &sm.range, sm.scratch);
+  split_range<kThreads>(cost, P.B, P.nc, blockIdx.x, 1, kItem + kMinPart, kMinPart, &sm.range, sm.scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -690,13 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
           }
           if (!row_ok) continue;
+          float x[16];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            float x[8];
-#pragma unroll
-            for (int t = 0; t < 8; ++t) x[t] = some ? __uint_as_float(raw[8 * v + t]) * inv : 0.f;
-            store8(dst + c + v * 8, x);
-          }
+          for (int t = 0; t < 16; ++t) x[t] = some ? __uint_as_float(raw[t]) * inv : 0.f;
+          store16(dst + c, x, P.wide);
         }
         if (row_ok && half == 0 && P.lse) P.lse[out] = some ? (m_ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
       } else {
@@ -830,6 +835,7 @@ ispa_status launch_attn_prompt(const ispa_attn_seq_desc &d, float scale, int Tq,
   P.Tk = Tk;
   P.causal = d.causal;
   P.nc = sm_count();
+  P.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   P.scale_log2 = scale * 1.4426950408889634f;
   P.cu_q = cu_q;
   P.cu_k = cu_k;

@@ -196,6 +196,40 @@ __device__ __forceinline__ void store8(__half *p, const float (&x)[8]) {
                                              pack_half2(x[6], x[7]));
 }
 
+// Sixteen values of a row that lies far from the neighbouring lanes' rows: whole 32-byte
+// sectors at a time when the address allows it (wide), else in 16-byte pieces.
+__device__ __forceinline__ void store32b(void *p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ void store16(float *p, const float (&x)[16], bool wide) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * h + i]);
+    store32b(p + 8 * h, w, wide);
+  }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&x)[16], bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  store32b(p, w, wide);
+}
+__device__ __forceinline__ void store16(__half *p, const float (&x)[16], bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+  store32b(p, w, wide);
+}
+
 __device__ __forceinline__ float2 unpack16(uint32_t w, const __half *) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }

@@ -255,6 +255,26 @@ def test_prompt_sharp_softmax():
     run_prompt(np.random.default_rng(6), 128, "fp16", torch.float32, 1, 2, [200, 900], [1500, 900], True, scale=1.5)
 
 
+def test_prompt_output_at_every_alignment_allowed():
+    """O 16-byte but not 32-byte aligned gives the same bits as an aligned one."""
+    rng = np.random.default_rng(12)
+    q, k, v = (rand16(rng, (150, h, 64), torch.bfloat16).cuda() for h in (2, 1, 1))
+    cu = ints([0, 150])
+    for out in (torch.bfloat16, torch.float32):
+        a = ispa.attn_seq_desc(1, 2, 1, 64, ispa.ISPA_BF16, CODE[out])
+        got = []
+        for shift in (0, 16):
+            n = shift // torch.empty(0, dtype=out).element_size()
+            buf = torch.full((150 * 2 * 64 + 16,), 7.0, dtype=out, device="cuda")
+            o = buf[n:n + 150 * 2 * 64].view(150, 2, 64)
+            assert o.data_ptr() % 32 == shift
+            ispa.ispa_attn_prompt(a, q, k, v, cu, cu, o, None, workspace=prompt_ws(a))
+            assert torch.all(buf[:n] == 7.0) and torch.all(buf[n + 150 * 2 * 64:] == 7.0)
+            got.append(o.clone())
+        assert torch.equal(*got)
+    ispa.ispa_check_device_error()
+
+
 def test_prompts_many_sequences():
     rng = np.random.default_rng(7)
     n = [int(x) for x in rng.integers(0, 30, 900)]
