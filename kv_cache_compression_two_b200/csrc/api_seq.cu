@@ -19,7 +19,7 @@ ispa_status check_cache(const ispa_kvq_desc *d) {
     return fail(ISPA_ERR_INVALID_ARG, "page_tokens must be 16, 32, 64, 128 or 256 (got %d)", d->page_tokens);
   if (d->fmt != ISPA_KVQ_E4M3 && d->fmt != ISPA_KVQ_INT8 && d->fmt != ISPA_KVQ_INT4)
     return fail(ISPA_ERR_INVALID_ARG, "bad cache format");
-  if ((long long)d->H_kv * d->page_tokens > (1LL << 31) || (long long)d->n_pages * d->H_kv > (1LL << 32))
+  if (d->H_kv > (1 << 16) || (long long)d->n_pages * d->H_kv > (1LL << 32))
     return fail(ISPA_ERR_INVALID_ARG, "cache too large");
   return ISPA_OK;
 }

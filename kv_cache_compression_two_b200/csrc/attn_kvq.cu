@@ -187,16 +187,28 @@ __device__ __forceinline__ void four_codes(uint32_t w, uint32_t &lo, uint32_t &h
         : "r"(w));
   }
 }
-// Nibble i of both 16-bit halves of a word as fp16 values (n - 8) f, exactly: with the nibble
-// in mantissa bits 4..7 of 1024 the fp16 number is 1024 + 16 n, and (1024 + 16 n) (f / 16) - 72 f
-// is one fused operation whose operands (f has 4 significant bits) and result (7) are fp16 numbers.
+// The four nibbles of both 16-bit halves of a word as fp16 values (n - 8) f, exactly.
+// A nibble in mantissa bits 4..7 of 1024 makes the fp16 number 1024 + 16 n, and
+// (1024 + 16 n) (f / 16) - 72 f is one fused operation whose operands (f has 4
+// significant bits) and result (7) are fp16 numbers; one in bits 0..3 makes 1024 + n, and
+// (1024 + n) - 1032, then times f, are two.  Taking nibbles 0 and 2 the second way costs one
+// shift a word instead of three: the integer pipe is the scarcer one here.
 struct Factor {
-  uint32_t sixteenth, minus72;  // pairs f / 16 and -72 f
-  __device__ __forceinline__ explicit Factor(uint32_t f) : sixteenth(hmul2(f, 0x2c002c00u)), minus72(hmul2(f, 0xd480d480u)) {}
+  uint32_t one, sixteenth, minus72;  // pairs f, f / 16 and -72 f
+  __device__ __forceinline__ explicit Factor(uint32_t f)
+      : one(f), sixteenth(hmul2(f, 0x2c002c00u)), minus72(hmul2(f, 0xd480d480u)) {}
 };
-__device__ __forceinline__ uint32_t two_nibbles(uint32_t w, int i, const Factor &f) {
-  const uint32_t at4 = i == 0 ? w << 4 : i == 1 ? w : w >> (4 * (i - 1));
-  return hfma2((at4 & 0x00f000f0u) | 0x64006400u, f.sixteenth, f.minus72);
+__device__ __forceinline__ uint32_t nibble_bits(uint32_t w, uint32_t mask) {
+  uint32_t r;  // (w & mask) | 0x64006400 in one operation
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+  return r;
+}
+__device__ __forceinline__ void four_nibbles(uint32_t w, const Factor &f, uint32_t (&n)[4]) {
+  const uint32_t u = w >> 8;
+  n[0] = hmul2(hsub2(nibble_bits(w, 0x000f000fu), 0x64086408u), f.one);
+  n[1] = hfma2(nibble_bits(w, 0x00f000f0u), f.sixteenth, f.minus72);
+  n[2] = hmul2(hsub2(nibble_bits(u, 0x000f000fu), 0x64086408u), f.one);
+  n[3] = hfma2(nibble_bits(u, 0x00f000f0u), f.sixteenth, f.minus72);
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
@@ -227,39 +239,55 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int half, const unsigned
   }
 }
 
+// Where one head's tiles lie: addresses of page 0, this lane's bytes; a page's stride.
+struct TileSource {
+  const unsigned char *k, *v, *rec;
+  uint32_t code_page, rec_page;
+  int mask;
+};
+
 template <int FMT, int D>
-__device__ __forceinline__ void load_tile(const KvqView &c, uint32_t dst, int h, int tok0, int len, int pg0, int pg1) {
+__device__ __forceinline__ TileSource tile_source(const KvqView &c, int h) {
   using Ge = Geo<FMT, D, 1>;
-  const int lane = threadIdx.x & 31;
-  const int mask = (1 << c.page_log2) - 1;
-  constexpr int RPI = 32 / Ge::CPR;
   constexpr int SC = Ge::REC;  // 16-byte pieces of 16 scale records
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)h << c.page_log2;
+  const uint32_t rows = (uint32_t)c.H_kv << c.page_log2;
+  return {c.k_code + row * Ge::ROW + lane * 16, c.v_code + row * Ge::ROW + lane * 16,
+          (lane < SC ? c.k_scale : c.v_scale) + row * Ge::REC + (lane % SC) * 16, rows * Ge::ROW, rows * Ge::REC,
+          (1 << c.page_log2) - 1};
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_tile(const TileSource &src, uint32_t dst, int tok0, int len, int pg0, int pg1) {
+  using Ge = Geo<FMT, D, 1>;
+  constexpr int RPI = 32 / Ge::CPR, SC = Ge::REC;
+  const int lane = threadIdx.x & 31;
   const int ch = lane % Ge::CPR, r0 = lane / Ge::CPR;
+  const uint32_t rec_dst = dst + 2 * Ge::CODE + (lane < SC ? 0 : Ge::SCALE) + (lane % SC) * 16;
   const bool full = tok0 + kTile <= len && (pg0 | pg1) >= 0;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int pg = half ? pg1 : pg0, t0 = tok0 + half * 16;
-    const long long row0 = c.row(pg < 0 ? 0 : pg, h, t0 & mask);
-    const uint32_t rec = dst + 2 * Ge::CODE + (lane < SC ? 0 : Ge::SCALE) + half * 16 * Ge::REC + (lane % SC) * 16;
-    const unsigned char *s = (lane < SC ? c.k_scale : c.v_scale) + row0 * Ge::REC;
+    const uint32_t page = pg < 0 ? 0u : (uint32_t)pg, place = t0 & src.mask;
+    const unsigned long long at = (unsigned long long)page * src.code_page + place * Ge::ROW;
+    const unsigned char *rec = src.rec + ((unsigned long long)page * src.rec_page + place * Ge::REC);
     if (full) {
-      const long long at = row0 * Ge::ROW + lane * 16;
-      copy_rows<FMT, D, 0>(dst, half, c.k_code + at, c.v_code + at, ch, r0);
-      if (lane < 2 * SC) cp_async16(rec, s + (lane % SC) * 16, 16);
+      copy_rows<FMT, D, 0>(dst, half, src.k + at, src.v + at, ch, r0);
+      if (lane < 2 * SC) cp_async16(rec_dst + half * 16 * Ge::REC, rec, 16);
     } else {
-      const unsigned char *ks = c.k_code + row0 * Ge::ROW, *vs = c.v_code + row0 * Ge::ROW;
 #pragma unroll
       for (int i = 0; i < 16 / RPI; ++i) {
         const int r = i * RPI + r0;
         const bool on = pg >= 0 && t0 + r < len;
-        const int off = on ? r * Ge::ROW + ch * 16 : 0;
-        cp_async16(dst + Ge::k_off(half * 16 + r, ch), ks + off, on ? 16 : 0);
-        cp_async16(dst + Ge::CODE + Ge::v_off(half * 16 + r, ch), vs + off, on ? 16 : 0);
+        const unsigned long long off = on ? at + i * RPI * Ge::ROW : 0ull;
+        cp_async16(dst + Ge::k_off(half * 16 + r, ch), src.k + off, on ? 16 : 0);
+        cp_async16(dst + Ge::CODE + Ge::v_off(half * 16 + r, ch), src.v + off, on ? 16 : 0);
       }
       if (lane < 2 * SC) {
         const int tok = t0 + (lane % SC) * (16 / Ge::REC);
         const int bytes = pg >= 0 ? min(16, max(0, (len - tok) * Ge::REC)) : 0;
-        cp_async16(rec, s + (bytes ? (lane % SC) * 16 : 0), bytes);
+        cp_async16(rec_dst + half * 16 * Ge::REC, bytes ? rec : src.rec, bytes);
       }
     }
   }
@@ -330,11 +358,12 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
       }
     };
     int np0, np1;
+    const TileSource src = tile_source<FMT, D>(P.c, h);
 #pragma unroll
     for (int s = 0; s < Ge::STAGES - 1; ++s) {
       const int tile = my0 + s * kWarps;
       pages(tile, np0, np1);
-      if (tile < t_end) load_tile<FMT, D>(P.c, ring_u + s * Ge::STAGE, h, tile * kTile, len, np0, np1);
+      if (tile < t_end) load_tile<FMT, D>(src, ring_u + s * Ge::STAGE, tile * kTile, len, np0, np1);
       cp_commit();
     }
     pages(my0 + (Ge::STAGES - 1) * kWarps, np0, np1);
@@ -411,7 +440,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
       {  // refill the stage read in the last round
         const int nt = tile + (Ge::STAGES - 1) * kWarps;
         const int ns = stage == 0 ? Ge::STAGES - 1 : stage - 1;
-        if (nt < t_end) load_tile<FMT, D>(P.c, ring_u + ns * Ge::STAGE, h, nt * kTile, len, np0, np1);
+        if (nt < t_end) load_tile<FMT, D>(src, ring_u + ns * Ge::STAGE, nt * kTile, len, np0, np1);
         cp_commit();
         pages(nt + kWarps, np0, np1);
       }
@@ -451,10 +480,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
           const Factor f0(e4m3x2_to_half2(prmt(rec0.y, 0u, pick))), f1(e4m3x2_to_half2(prmt(rec1.y, 0u, pick)));
 #pragma unroll
           for (int i = 0; i < WORDS; ++i) {
-            const uint4 a0 = make_uint4(two_nibbles(w[0][i], 0, f0), two_nibbles(w[1][i], 0, f1),
-                                        two_nibbles(w[0][i], 1, f0), two_nibbles(w[1][i], 1, f1));
-            const uint4 a1 = make_uint4(two_nibbles(w[0][i], 2, f0), two_nibbles(w[1][i], 2, f1),
-                                        two_nibbles(w[0][i], 3, f0), two_nibbles(w[1][i], 3, f1));
+            uint32_t n0[4], n1[4];
+            four_nibbles(w[0][i], f0, n0);
+            four_nibbles(w[1][i], f1, n1);
+            const uint4 a0 = make_uint4(n0[0], n1[0], n0[1], n1[1]), a1 = make_uint4(n0[2], n1[2], n0[3], n1[3]);
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
               mma16816(s[tb][nr], a0, qb[2 * i][nr].x, qb[2 * i][nr].y);
@@ -612,10 +641,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
             for (int hw = 0; hw < 2; ++hw) {  // 16-bit halves of the words: channels 0-3, 4-7
               const uint32_t xa = prmt(w[0][i], w[1][i], hw ? 0x7632 : 0x5410);
               const uint32_t xb = prmt(w[2][i], w[3][i], hw ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int c = 0; c < 4; c += 2)
-                product(i * 4 + hw * 2 + c / 2, kb, two_nibbles(xa, c, fa), two_nibbles(xa, c + 1, fa),
-                        two_nibbles(xb, c, fb), two_nibbles(xb, c + 1, fb));
+              uint32_t na[4], nb[4];
+              four_nibbles(xa, fa, na);
+              four_nibbles(xb, fb, nb);
+              product(i * 4 + hw * 2, kb, na[0], na[1], nb[0], nb[1]);
+              product(i * 4 + hw * 2 + 1, kb, na[2], na[3], nb[2], nb[3]);
             }
         } else {
           constexpr int WORDS = D / 32;
