@@ -346,14 +346,25 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
     // ---- this warp's first tiles are on their way while Q is laid out
     const int my0 = t_begin + warp;
     int bad = 0;
+    // pages of a tile's two halves, -1 where there is none (a tile below the length lies inside the table)
+    const int *table = P.c.table + (long long)b * P.c.max_pages;
+    const int page_log2 = P.c.page_log2;
+    const unsigned n_pages = P.c.n_pages;
     auto pages = [&](int tile, int &p0, int &p1) {
       p0 = p1 = -1;
-      if (tile < t_end && tile * kTile < len) {
-        p0 = P.c.page(b, tile * kTile);
-        bad |= p0 < 0;
-        if (tile * kTile + 16 < len) {
-          p1 = P.c.page(b, tile * kTile + 16);
-          bad |= p1 < 0;
+      const int tok = tile * kTile;
+      if (tile < t_end && tok < len) {
+        const int *at = table + (tok >> page_log2);
+        p0 = __ldg(at);
+        if ((unsigned)p0 >= n_pages) p0 = -1;
+        bad |= p0;
+        if (tok + 16 < len) {
+          p1 = p0;
+          if (page_log2 == 4) {
+            p1 = __ldg(at + 1);
+            if ((unsigned)p1 >= n_pages) p1 = -1;
+            bad |= p1;
+          }
         }
       }
     };
@@ -528,7 +539,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
               if (tok + (i >> 1) * 8 >= lim[nr][i & 1]) s[tb][nr][i] = kNegInf;
         }
       }
-      if (bad) {  // tokens whose page does not exist are left out
+      if (bad < 0) {  // tokens whose page does not exist are left out
         int p0, p1;
         const int keep = bad;
         pages(tile, p0, p1);
@@ -674,7 +685,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
         }
       }
     }
-    if (bad && lane == 0) report_seq(P.err, b);
+    if (bad < 0 && lane == 0) report_seq(P.err, b);
 
     // ---- merge the warps' states (the rings are idle now)
     cp_wait<0>();
