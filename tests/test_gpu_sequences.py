@@ -246,6 +246,12 @@ def test_prompts_split_over_sms(d, dtype, causal):
     run_prompt(np.random.default_rng(2), d, dtype, torch.float32, 1, 1, [33, 300], [12011, 5001], causal)
 
 
+@pytest.mark.parametrize("d,B,H_kv,nq,nk", [(64, 2, 9, 2300, 515), (128, 1, 13, 3001, 2100), (128, 3, 1, 300, 700)])
+def test_prompts_alike_over_every_key(d, B, H_kv, nq, nk):
+    """Equal sequences that see every key: more items than SMs (whole rounds, then a cut rest), or fewer."""
+    run_prompt(np.random.default_rng(13), d, "bf16", torch.float32, 1, H_kv, [nq] * B, [nk] * B, False)
+
+
 def test_prompt_long_causal():
     run_prompt(np.random.default_rng(5), 128, "bf16", torch.bfloat16, 4, 1, [3001], [3001], True, fused=True)
 
