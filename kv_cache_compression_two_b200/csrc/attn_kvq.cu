@@ -68,15 +68,17 @@ constexpr int part_floats() { return 8 * NR * (D + 2); }
 // Steps of a sequence: tiles x row blocks x heads.
 struct KvqCost {
   const int *cu, *lens;
-  int T, cap, G, H_kv, rows;  // rows: of a block
-  __device__ int blocks(int b) const { return (int)(((long long)seq_rows(cu, b, T).n * G + rows - 1) / rows); }
+  int T, cap, G, H_kv, rows_log2;  // rows of a block
+  __device__ int blocks(int b) const {
+    return (int)(((long long)seq_rows(cu, b, T).n * G + (1 << rows_log2) - 1) >> rows_log2);
+  }
   __device__ int tiles(int b) const { return max(1, (seq_len(lens, b, cap) + kTile - 1) / kTile); }
   // An item costs its tiles and about kItem more: the first tiles' latency, laying out Q, merging the warps.
   __device__ int steps(int b) const { return tiles(b) + kItem; }
   __device__ long long cost(int b) const { return (long long)blocks(b) * H_kv * steps(b); }
   __device__ int item(int b, long long off, long long *s, long long *e) const {
     const int t = steps(b);
-    *s = off / t * t;
+    *s = div_pos(off, t) * t;
     *e = *s + t;
     return 0;
   }
@@ -308,12 +310,12 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
   constexpr bool kTwoParts = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ SplitRange range;
-  __shared__ long long scratch[kWarps + 6];
+  __shared__ long long scratch[kWarps + 8];
   __shared__ float q_unscale[kRows];
   unsigned char *qh = smem + (Ge::RING > Ge::MERGE ? Ge::RING : Ge::MERGE);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const KvqCost cost = {P.cu, P.lens, P.T, P.cap, P.G, P.c.H_kv, kRows};
+  const KvqCost cost = {P.cu, P.lens, P.T, P.cap, P.G, P.c.H_kv, NR == 1 ? 3 : 4};
   asm volatile("griddepcontrol.launch_dependents;");  // the merge may take its place on the SMs; it waits for this grid
   if (threadIdx.x < 2) P.meta[2 * blockIdx.x + threadIdx.x].state = 0;
   if (blockIdx.x == 0)
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
     }
     const int len = seq_len(P.lens, b, P.cap);
     // step x of an item is its tile x - kItem (a boundary lies at x = 0 or well behind kItem)
-    const int item = (int)(off / steps), x_begin = (int)(off % steps);
+    const int item = (int)div_pos(off, steps), x_begin = (int)(off - (long long)item * steps);
     const int x_end = (int)min((long long)steps, x_begin + left);
     const int t_begin = max(0, x_begin - kItem), t_end = max(0, x_end - kItem);
     const int h = item / blocks, rb = item % blocks;

@@ -124,8 +124,23 @@ struct PromptCost {
   __device__ long long tiles_before(const PromptSeq &s, int pair) const {
     if (!causal) return (long long)pair * max(1, (s.len + kTile - 1) >> 7);
     const int R = 2 * TQ;
-    const int ones = min(pair, s.past >= kTile ? 0 : (kTile - s.past) / R);  // pairs of one step
-    return ones + floor_sum(pair - ones, kTile, R, (uint32_t)(s.past + (ones + 1) * R + kTile - 1));
+    const bool pow2 = (R & (R - 1)) == 0;  // (as for every group of 2^k heads; the general sum is several divisions)
+    const int lg = 31 - __clz(R);
+    const int room = kTile - s.past;
+    const int ones = min(pair, room <= 0 ? 0 : pow2 ? room >> lg : room / R);  // pairs of one step
+    const int n = pair - ones;
+    if (n == 0) return ones;
+    const uint32_t b = s.past + (ones + 1) * R + kTile - 1;
+    if (pow2) {
+      if (R >= kTile) return ones + (long long)(R >> 7) * n * (n - 1) / 2 + (long long)n * (b >> 7);
+      const int per = 7 - lg;  // floor((R i + b) / 128) = floor((i + floor(b / R)) / 2^per)
+      auto sum = [per](long long x) {  // of floor(j / 2^per) over j < x
+        const long long q = x >> per;
+        return ((q * (q - 1) / 2) << per) + q * (x - (q << per));
+      };
+      return ones + sum((b >> lg) + n) - sum(b >> lg);
+    }
+    return ones + floor_sum(n, kTile, R, b);
   }
   __device__ long long head(const PromptSeq &s) const {
     return s.pairs ? before(s, s.pairs - 1) + steps(s, s.pairs - 1) : 0;
@@ -135,7 +150,7 @@ struct PromptCost {
   __device__ int item(int b, long long off, long long *s, long long *e) const {
     const PromptSeq q = seq(b);
     const long long line = head(q);
-    const int h = (int)(off / line);
+    const int h = (int)div_pos(off, line);
     const long long rem = off - h * line;
     int lo = 0, n = q.pairs;
     const int lane = threadIdx.x & 31;
@@ -282,7 +297,7 @@ struct PromptSmem {
   float swap[2][2][kTile];  // per tile: what the two threads of a row tell each other
   PromptSeg seg[kSegs];
   PromptWalk walk;
-  long long scratch[kThreads / 32 + 6];
+  long long scratch[kThreads / 32 + 8];
   SplitRange range;
   uint32_t tmem_base;
   int abort;

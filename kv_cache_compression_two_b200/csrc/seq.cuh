@@ -61,6 +61,17 @@ __device__ __forceinline__ int seq_of_row(const int *cu, int B, int t) {
   return n > 0 && lo < B && __ldg(cu + lo) <= t ? lo : -1;
 }
 
+// a b / n and a / b; in 32 bits where they fit (64-bit division is a long routine, and these
+// stand in front of a call's first load).
+__device__ __forceinline__ long long mul_div(int a, long long b, int n) {
+  if (b < (1LL << 32) / 2048 && a < 2048) return (uint32_t)a * (uint32_t)b / (uint32_t)n;
+  return a * b / n;
+}
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  if (a < (1LL << 32) && b < (1LL << 32)) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 struct SplitRange {
   int b;             // sequence that holds the first step
   int tag;           // f.item()'s name of the item
@@ -72,7 +83,7 @@ struct SplitRange {
 // This CTA's stretch.  f.cost(b): steps of sequence b; f.item(b, off, &s, &e)
 // (called by a whole warp): the item [s, e) that holds step off of sequence b.
 // At most ceil(total / min_unit) CTAs get work.  Called by all NT threads; sw:
-// NT / 32 + 6 values of scratch.
+// NT / 32 + 8 values of scratch.
 template <int NT, class F>
 __device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int min_head, int min_tail, SplitRange *r,
                             long long *sw) {
@@ -91,30 +102,39 @@ __device__ void split_range(const F &f, int B, int nc, int c, int min_unit, int 
   long long *found = sw + NT / 32;  // per boundary: sequence (-1: none), place in it, place of the sequence
   if (tid < 2) found[3 * tid] = -1;
   __syncthreads();
-  long long pre = inc - mine, total = 0;
+  if (warp == 0) {  // the warps' sums to prefixes; the line's length; the two boundaries, before they
+                    // move to an item's edge (none: 0 or the end of the line)
+    const long long own = lane < NT / 32 ? sw[lane] : 0;
+    long long up_to = own;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) pre += sw[w];
-    total += sw[w];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, up_to, o);
+      if (lane >= o) up_to += up;
+    }
+    const long long total = __shfl_sync(0xffffffffu, up_to, 31);
+    if (lane < NT / 32) sw[lane] = up_to - own;
+    const long long want = min_unit == 1 ? total : div_pos(total + min_unit - 1, min_unit);
+    const int n = (int)(want < nc ? (want > 0 ? want : 1) : nc);
+    if (lane < 2) found[6 + lane] = c < n ? mul_div(c + lane, total, n) : total;
+    if (lane == 0) {
+      r->b = 0;
+      r->tag = 0;
+      r->off = 0;
+      r->begin = 0;
+      r->x0 = c < n ? 0 : total;
+      r->x1 = total;
+    }
   }
-  const long long want = (total + min_unit - 1) / min_unit;
-  const int n = (int)(want < nc ? (want > 0 ? want : 1) : nc);
-  if (tid == 0) {
-    r->b = 0;
-    r->tag = 0;
-    r->off = 0;
-    r->begin = 0;
-    r->x0 = c < n ? 0 : total;
-    r->x1 = total;
-  }
-  if (c < n) {
+  __syncthreads();
+  const long long pre = sw[warp] + inc - mine, total = r->x1;
+  if (mine > 0) {
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-      const long long x = (long long)(c + k) * total / n;
+      const long long x = found[6 + k];
       if (x <= 0 || x >= total || x < pre || x >= pre + mine) continue;
       long long p = pre;
       for (int b = b0; b < b1; ++b) {
-        const long long cb = f.cost(b);
+        const long long cb = b1 - b0 == 1 ? mine : f.cost(b);
         if (x < p + cb) {
           found[3 * k] = b;
           found[3 * k + 1] = x - p;
