@@ -584,7 +584,7 @@ ispa_status ispa_attn_local_proj_q8(const ispa_attn_desc *desc, const void *q, c
  * K, V and Q rows may be strided: row t of k starts at k + t * k_stride
  * elements (k_stride >= H_kv * head_dim, a multiple of 8), with the row's
  * heads back to back, so that they can be slices of a fused projection.
- * Outputs are contiguous.  head_dim is 64 or 128.
+ * Outputs are contiguous and overlap no input.  head_dim is 64 or 128.
  */
 
 /* How the cache stores a row (one token of one head of K or of V, d values x). */
@@ -653,13 +653,15 @@ typedef struct {
  * tokens.  Sequence b's queries are the rows [cu_q[b], cu_q[b+1]) of q
  * [T, H, d], its keys the first seq_lens[b] tokens of its cache; with causal,
  * the queries are its last tokens (already written).  Any number of query
- * tokens is taken; the cache is read once per 16 rows of tokens * (H / H_kv).
+ * tokens is taken; the cache is read once per 8 rows of tokens * (H / H_kv) when
+ * there are no more than 8 to a sequence on the average, else once per 16.
  *   o    [T, H, d] out_dtype, lse [T, H] fp32 or NULL.  A query that sees no
  *        key gives O = 0, lse = -inf.
  *   Arithmetic: q in fp16 scaled by a power of two per row (exact for entries
  *   above 2^-29 of the row's largest), codes exactly in fp16, products
  *   accumulated in fp32; softmax statistics in fp32; the weights, times the
- *   V scale, enter the second product in fp16 (11 significant bits).
+ *   V scale, enter the second product in fp16 (11 significant bits; for fp16
+ *   inputs as the sum of two fp16 numbers).
  *   workspace >= ispa_attn_kvq_workspace_bytes(...), 16-byte aligned: partial
  *   results of sequences that several SMs share.  Calls (or captured graphs)
  *   that may run at the same time need one each.  The same inputs give the

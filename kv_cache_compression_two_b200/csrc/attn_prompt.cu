@@ -7,33 +7,48 @@
 // every K/V tile, short sequences fill the tiles better, and a causal tile's
 // diagonal is 128 / group tokens wide.
 //
-// Warps (384 threads):
-//   0      TMA producer: the pair's Q tiles, then K_0, V_0, K_1, V_1, ... through
-//          one ring of stages
-//   1      TMEM allocator and MMA issuer (whole warp; one lane issues)
-//   2      scheduler: walks the stretch and hands the items on through a ring in shared memory, so that
-//          no role on the critical path holds the walk's state (when every role walked for itself, the
-//          spilled registers went to L2 -- shared memory leaves no L1 -- and a step took 14 k cycles)
-//   3      idle
-//   4-7    softmax and output of tile A, one row per thread (TMEM lane = row)
-//   8-11   the same for tile B
+// Warps (640 threads):
+//   0-7    softmax and output of tile A: two threads a row (TMEM lane = row), 64 keys and
+//          half of O's columns each; they exchange maxima and sums through shared memory
+//   8-15   the same for tile B
+//   16     TMA producer: the pair's Q tiles, then K_0, V_0, K_1, V_1, ... through one ring
+//   17     TMEM allocator and MMA issuer (warp-uniform code, an elected lane issues)
+//   18     scheduler: walks the stretch and hands the items on through a ring in shared
+//          memory, so that no role on the critical path holds the walk's state (when every role
+//          walked for itself, the spilled registers went to L2 -- shared memory leaves no
+//          L1 -- and a step took 14 k cycles)
+//   19     idle
 // TMEM: S of A [0,128), S of B [128,256), O of A [256,256+d), O of B [384,384+d).
-// P overwrites the first 64 columns of its S.  The issuer's order is
+// P overwrites the first half of each thread's 64 score columns and is published in two
+// parts (16-key steps 0 1 4 5, then 2 3 6 7), so that the second product starts while the
+// second part is formed.  The issuer's order is
 //   S_A0 S_B0 | PV_A0 S_A1 | PV_B0 S_B1 | PV_A1 S_A2 | ...
-// so while one warpgroup works on its scores the tensor cores run the other
-// tile's two products: the softmax's latency chain, which bounds a kernel with
-// one tile in flight, is hidden behind the other tile.  Q and K come from
-// shared memory (S is SS, PV is TS): measured by itself the pair S + PV of a
-// 128 x 128 x 128 tile takes 1204 cycles against 1024 at the nominal rate, and
-// keeping Q in TMEM instead would leave no room for the second tile.
+// so while one tile's warps work on its scores the tensor cores run the other tile's two
+// products: the softmax's latency chain, which bounds a kernel with one tile in flight, is
+// hidden behind the other tile.  Q and K come from shared memory (S is SS, PV is TS): a
+// probe of the pair S + PV of a 128 x 128 x 128 tile back to back takes 1025 cycles, the
+// nominal rate, with the TMEM loads and copies of the other roles running or not.
+//
+// What bounds it: a step takes about 3300 cycles for 2050 of MMAs.  The chain of a tile
+// is 410 (scores in, maximum, exchange) + 190 + 2 x 680 (exponentials of 32 columns, two
+// warps an SM sub-partition: 0.75 of the MUFU rate) + 230 until the weights are published,
+// then 100 to the issuer and about 1000 for the products; the two tiles' exponentials
+// nearly fill the MUFU.  Tried: an eighth to a half of the exponentials as polynomials on
+// the FMA pipe (the same to 10 % slower), one thread a row with the scores in registers
+// (spills), spinning waits, one pass over the scores with a late correction (spills).
+//
+// Measured (bf16, d = 128): 8192 causal tokens, 32 heads on 8, 455 us, 1210 TFLOP/s (0.72
+// of the measured burst peak, 0.86 of the sustained one); 4680 queries over 32760 keys, 12
+// heads, 742 us alone, 1270 TFLOP/s; six prompts of 545 to 2815 tokens 164 us, 850
+// TFLOP/s; 24 prompts of 1 to 300 tokens (d = 64) 14.3 us.
 //
 // Ordering (MMAs of one thread execute in order; a commit fires when all
 // earlier ones have completed): S_{j+1} is issued after PV_j of the same tile,
 // so it may overwrite P_j, and s_full(j + 1) says that O holds PV_0..PV_j: a
 // softmax warp that has seen it may rescale O without a further wait, PV_{j+1}
-// being held back by p_full(j + 1).  The last PV of an item commits o_final;
-// the next item's first PV overwrites O after the p_full that the same
-// warpgroup publishes behind its reading of O.
+// being held back by p_half(j + 1), which every warp of the tile signs.  The last
+// PV of an item commits o_final; the next item's first PV overwrites O after the
+// p_half that the same warps publish behind their reading of O.
 //
 // Keys: a tile past the end of its sequence holds rows of the next one, or
 // zeros.  Scores there are replaced by -inf; in the second product only the
@@ -799,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
-      tc_fence_before();  // O is read before the p_full that lets the next item overwrite it
+      tc_fence_before();  // O is read before the p_half that lets the next item overwrite it
     }
   }
   tc_fence_before();
