@@ -351,7 +351,18 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
     const int t_begin = max(0, x_begin - kItem), t_end = max(0, x_end - kItem);
     const int h = item / blocks, rb = item % blocks;
     const int n_rows = min(kRows, rows.n * P.G - rb * kRows);
-    // ---- this warp's first tiles are on their way while Q is laid out
+    // ---- all loads of the start are issued together: Q's rows, the first tiles' pages, then the tiles,
+    // which are on their way while Q is laid out
+    constexpr int PER = D / 32, kMine = kRows / kWarps;  // values of a row per lane, rows of a warp
+    uint32_t qw[kMine][PER / 2];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int r = warp + i * kWarps, rr = rb * kRows + r;
+      const T *src = static_cast<const T *>(P.q) + (long long)(rows.begin + rr / P.G) * P.qs +
+                     (long long)(h * P.G + rr % P.G) * D + lane * PER;
+#pragma unroll
+      for (int k = 0; k < PER / 2; ++k) qw[i][k] = r < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(src) + k) : 0u;
+    }
     const int my0 = t_begin + warp;
     int bad = 0;
     // pages of a tile's two halves, -1 where there is none (a tile below the length lies inside the table)
@@ -376,42 +387,36 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
         }
       }
     };
-    int np0, np1;
     const TileSource src = tile_source<FMT, D>(P.c, h);
+    int fp[Ge::STAGES][2];
+#pragma unroll
+    for (int s = 0; s < Ge::STAGES; ++s) pages(my0 + s * kWarps, fp[s][0], fp[s][1]);
 #pragma unroll
     for (int s = 0; s < Ge::STAGES - 1; ++s) {
       const int tile = my0 + s * kWarps;
-      pages(tile, np0, np1);
-      if (tile < t_end) load_tile<FMT, D>(src, ring_u + s * Ge::STAGE, tile * kTile, len, np0, np1);
+      if (tile < t_end) load_tile<FMT, D>(src, ring_u + s * Ge::STAGE, tile * kTile, len, fp[s][0], fp[s][1]);
       cp_commit();
     }
-    pages(my0 + (Ge::STAGES - 1) * kWarps, np0, np1);
+    int np0 = fp[Ge::STAGES - 1][0], np1 = fp[Ge::STAGES - 1][1];
 
     // ---- Q: the rows as fp16, scaled by a power of two per row, in operand order
-    for (int r = warp; r < kRows; r += kWarps) {
-      constexpr int PER = D / 32;
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int r = warp + j * kWarps;
       float x[PER];
       float am = 0.f;
-      const int rr = rb * kRows + r;
-      if (r < n_rows) {
-        const int tok = rows.begin + rr / P.G, head = h * P.G + rr % P.G;
-        const T *src = static_cast<const T *>(P.q) + (long long)tok * P.qs + (long long)head * D + lane * PER;
 #pragma unroll
-        for (int i = 0; i < PER / 2; ++i) {
-          const float2 f = unpack16(__ldg(reinterpret_cast<const uint32_t *>(src) + i), static_cast<const T *>(nullptr));
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] = 0.f;
+      for (int i = 0; i < PER / 2; ++i) {
+        const float2 f = unpack16(qw[j][i], static_cast<const T *>(nullptr));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+        am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
       }
-#pragma unroll
-      for (int i = 0; i < PER; ++i) am = fmaxf(am, fabsf(x[i]));
       am = warp_max(am);
-      // largest entry in [2^14, 2^15); rows of zeros and non-finite rows stay as they are
-      const int e = am > 0.f && am < INFINITY ? min(14 - ilogbf(am), 126) : 0;
-      const float up = ldexpf(1.f, e);
+      // largest entry in [2^14, 2^15) (the exponent field; 2^126 at most); rows of zeros and
+      // non-finite rows stay as they are
+      const int e = am > 0.f && am < INFINITY ? min(14 + 127 - (int)(__float_as_uint(am) >> 23), 126) : 0;
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         int ks, t, half, el;
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
         reinterpret_cast<__half *>(qh)[(((ks * NR + (r >> 3)) * 32 + (r & 7) * 4 + t) * 2 + half) * 2 + el] =
             __float2half_rn(x[i] * up);
       }
-      if (lane == 0) q_unscale[r] = P.scale_log2 * ldexpf(1.f, -e);
+      if (lane == 0) q_unscale[r] = P.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
     }
     __syncthreads();
     uint2 qb[Ge::KS][NR];
