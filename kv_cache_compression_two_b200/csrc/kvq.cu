@@ -68,6 +68,26 @@ __device__ __forceinline__ float exact_e4m3(float a, float b, float inv) {
   return copysignf(fmaf(fmaf(-t, b, a), inv, t), a);  // (the sign of zero is kept)
 }
 
+// Sixteen codes rint(49 / 64 x / b) + 8, clamped if they may pass 7.  Two nibbles are joined
+// as floats (n0 + 16 n1 + 136 in the last byte of 1.5 * 2^23 + that): integer operations are scarcer.
+template <bool CLAMP>
+__device__ __forceinline__ uint4 nibbles(const float (&x)[16], float b, float inv) {
+  uint32_t byte[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float n[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float y = exact_half(x[2 * i + k] * (49.f / 64.f), b, inv);
+      if (CLAMP) y = fminf(fmaxf(y, -7.f), 7.f);
+      n[k] = __fadd_rn(y, 12582912.f);  // 1.5 * 2^23: rounds to the nearest even integer
+    }
+    byte[i] = __float_as_uint(fmaf(__fadd_rn(n[1], -12582912.f), 16.f, __fadd_rn(n[0], 136.f)));
+  }
+  return make_uint4(__byte_perm(__byte_perm(byte[0], byte[1], 0x40), __byte_perm(byte[2], byte[3], 0x40), 0x5410),
+                    __byte_perm(__byte_perm(byte[4], byte[5], 0x40), __byte_perm(byte[6], byte[7], 0x40), 0x5410), 0u, 0u);
+}
+
 // Sixteen values of a row of W lanes: codes (16 or 8 bytes) and the row's scale record.
 template <int FMT, int W>
 __device__ __forceinline__ void quantise16(const float (&x)[16], uint4 &code, uint2 &rec) {
@@ -88,15 +108,9 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], uint4 &code, ui
     const uint32_t g8 = some ? e4m3x2(exact_e4m3(ga, gb, ginv), 0.f) & 0xffu : 0u;
     const bool on = g8 != 0;
     const float b = on ? gb * e4m3x2_to_float(g8).x * 0.125f : 1.f;  // 3136 x / (amax g) = (49 / 64 x) / b
-    const float inv = reciprocal(b);
-    uint32_t c[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float n = fminf(fmaxf(exact_half(x[i] * (49.f / 64.f), b, inv), -7.f), 7.f);
-      // + 8, rounded to the nearest even integer by the addition of 1.5 * 2^23
-      c[i >> 3] |= (on ? __float_as_uint(n + 12582920.f) & 15u : 8u) << (4 * (i & 7));
-    }
-    code = make_uint4(c[0], c[1], 0u, 0u);
+    const float inv = on ? reciprocal(b) : 0.f;                      // (0: every n is 0)
+    // |n| <= 7 / (1 - 2^-4) < 7.5 unless g is below its type's normal numbers
+    code = __any_sync(0xffffffffu, g8 - 1u < 7u) ? nibbles<true>(x, b, inv) : nibbles<false>(x, b, inv);
     // the factors of the row's groups (two lanes hold each)
     uint32_t factors = g8 << (8 * ((threadIdx.x & (W - 1)) >> 1));
 #pragma unroll
