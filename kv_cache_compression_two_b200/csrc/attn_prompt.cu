@@ -482,6 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 16) {
+    // 128 x 64 + 512 x 104 registers: the 640 x 96 of the launch, and no spill in the softmax's loop
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 18) {
       // ---------------------------------------------------------- scheduler
       if (lane == 0) {
@@ -655,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     const int w = warp >> 3, half = (warp >> 2) & 1;
     const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
     const int tok = r / P.G, head = r % P.G;
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = P.causal ? g->lim + t : g->len;
       const int lim_first = P.causal ? g->lim + w * P.TQ : g->len;
       const int j0 = g->j0, end = g->end[w], mode = g->mode, slot = 2 * blockIdx.x + g->slot;
-      const long long out = (long long)(g->q_row + (row_ok ? t : 0)) * P.H + g->h * P.G + head;
+      const int out_row = g->q_row + (row_ok ? t : 0), out_head = g->h * P.G + head;
       __syncwarp();
       if (lane == 0) seg_done();
       else ++n_seg;
@@ -777,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool some = l > 0.f;
       if (mode == 1) {
         const float inv = some ? 1.f / l : 0.f;
+        const long long out = (long long)out_row * P.H + out_head;
         TO *dst = static_cast<TO *>(P.o) + out * D + half * (D / 2);
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 16) {
