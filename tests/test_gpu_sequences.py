@@ -246,7 +246,8 @@ def test_prompts_split_over_sms(d, dtype, causal):
     run_prompt(np.random.default_rng(2), d, dtype, torch.float32, 1, 1, [33, 300], [12011, 5001], causal)
 
 
-@pytest.mark.parametrize("d,B,H_kv,nq,nk", [(64, 2, 9, 2300, 515), (128, 1, 13, 3001, 2100), (128, 3, 1, 300, 700)])
+@pytest.mark.parametrize("d,B,H_kv,nq,nk", [(64, 2, 9, 2300, 515), (128, 1, 13, 3001, 2100), (128, 3, 1, 300, 700),
+                                            (64, 2, 3, 50, 0)])
 def test_prompts_alike_over_every_key(d, B, H_kv, nq, nk):
     """Equal sequences that see every key: more items than SMs (whole rounds, then a cut rest), or fewer."""
     run_prompt(np.random.default_rng(13), d, "bf16", torch.float32, 1, H_kv, [nq] * B, [nk] * B, False)
@@ -450,6 +451,109 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for (s, q, k, v, o, ws), want in zip(work, alone):
         assert torch.equal(o, want)
+    ispa.ispa_check_device_error()
+
+
+def test_graph_of_a_chunk_replayed_with_other_lengths():
+    """Write, read back and prompt attention captured once, replayed as the bounds on the device change."""
+    rng = np.random.default_rng(61)
+    H, H_kv, d, page, t = 6, 2, 128, 32, torch.bfloat16
+    T, Tk = 200, 1500
+    cd = ispa.kvq_desc(H_kv, d, page, 64, ispa.ISPA_KVQ_INT4)
+    kvq = torch.zeros(ispa.ispa_kvq_bytes(cd), dtype=torch.uint8, device="cuda")
+    table = ints(rng.permutation(64).reshape(2, 32))
+    x = torch.zeros(T, H + 2 * H_kv, d, dtype=t, device="cuda")
+    a = ispa.attn_seq_desc(2, H, H_kv, d, ispa.ISPA_BF16, ispa.ISPA_F32)
+    cu_q, cu_k, lens = ints([0, 0, 0]), ints([0, 0, 0]), ints([0, 0])
+    kb, vb = (torch.zeros(Tk, H_kv, d, dtype=t, device="cuda") for _ in range(2))
+    o, ws = torch.zeros(T, H, d, device="cuda"), prompt_ws(a)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        ispa.ispa_kvq_write(cd, x[:, H:H + H_kv], x[:, H + H_kv:], table, lens, cu_q, kvq)
+        ispa.ispa_kvq_read(cd, kvq, table, cu_k, kb, vb)
+        ispa.ispa_attn_prompt(a, x[:, :H], kb, vb, cu_q, cu_k, o, None, workspace=ws)
+    total = np.zeros(2, int)
+    oc = so.Cache("int4", H_kv, d, page, 64)
+    htab = table.cpu().numpy()
+    for new in ([150, 50], [0, 200], [33, 1], [100, 100]):
+        y = rand16(rng, (T, H + 2 * H_kv, d), t)
+        total = total + new
+        cq, ck = starts(new), starts(total)
+        x.copy_(y)
+        cu_q.copy_(ints(cq)), cu_k.copy_(ints(ck)), lens.copy_(ints(total))
+        graph.replay()
+        ispa.ispa_check_device_error()
+        for b in range(2):
+            z = y[cq[b]:cq[b + 1]]
+            oc.put(htab[b], np.arange(total[b] - new[b], total[b]), f64(z[:, H:H + H_kv]), f64(z[:, H + H_kv:]))
+            k, v = (f64(torch.from_numpy(w).to(t)) for w in oc.get(htab[b], np.arange(total[b])))
+            if new[b]:
+                check_attention(o[cq[b]:cq[b + 1]], None, so.attention(f64(z[:, :H]), k, v, True), HALF[t], d,
+                                total[b], np.abs(v).max())
+
+
+def test_rows_in_front_of_the_first_sequence_stay():
+    """cu[0] > 0: the rows before it belong to no sequence."""
+    rng = np.random.default_rng(62)
+    k, v = (rand16(rng, (30, 1, 64), torch.bfloat16) for _ in range(2))
+    q = rand16(rng, (30, 2, 64), torch.bfloat16)
+    cu = ints([7, 12, 25])
+    a = ispa.attn_seq_desc(2, 2, 1, 64, ispa.ISPA_BF16, ispa.ISPA_F32)
+    o = torch.full((30, 2, 64), 7.0, device="cuda")
+    ispa.ispa_attn_prompt(a, q.cuda(), k.cuda(), v.cuda(), cu, cu, o, None, workspace=prompt_ws(a))
+    cd = ispa.kvq_desc(1, 64, 16, 3, ispa.ISPA_KVQ_E4M3)
+    c = so.Cache("e4m3", 1, 64, 16, 3, fill=0xAB)
+    kvq, table = cuda(c.buf.copy()), ints([[2], [0]])
+    ispa.ispa_kvq_write(cd, k.cuda(), v.cuda(), table, ints([5, 13]), cu, kvq)
+    c.put([2], np.arange(5), f64(k[7:12]), f64(v[7:12]))
+    c.put([0], np.arange(13), f64(k[12:25]), f64(v[12:25]))
+    assert np.array_equal(kvq.cpu().numpy(), c.buf)
+    o2 = torch.full((30, 2, 64), 7.0, device="cuda")
+    ispa.ispa_attn_kvq(a, cd, q.cuda(), kvq, table, ints([5, 13]), cu, o2, None, workspace=attn_ws(a, cd))
+    for rows, tab in ((slice(7, 12), [2]), (slice(12, 25), [0])):
+        n = rows.stop - rows.start
+        check_attention(o[rows], None, so.attention(f64(q[rows]), f64(k[rows]), f64(v[rows]), True), 2.0 ** -8, 64, n, 5.0)
+        kk, vv = c.get(tab, np.arange(n))
+        check_attention(o2[rows], None, so.attention(f64(q[rows]), kk, vv, True), 2.0 ** -11, 64, n, np.abs(vv).max() * 2 ** 7)
+    for x in (o, o2):
+        assert torch.all(x[:7] == 7.0) and torch.all(x[25:] == 7.0)
+    ispa.ispa_check_device_error()
+
+
+def test_no_rows_and_no_keys():
+    a = ispa.attn_seq_desc(1, 2, 1, 64, ispa.ISPA_F16, ispa.ISPA_F16)
+    none = torch.zeros(0, 1, 64, dtype=torch.float16, device="cuda")
+    q = torch.ones(3, 2, 64, dtype=torch.float16, device="cuda")
+    o, lse = torch.full_like(q, 7.0), torch.full((3, 2), 7.0, device="cuda")
+    ispa.ispa_attn_prompt(a, q, none, none, ints([0, 3]), ints([0, 0]), o, lse, workspace=prompt_ws(a))
+    assert torch.all(o == 0) and torch.all(lse == -float("inf"))
+    ispa.ispa_attn_prompt(a, q[:0], none, none, ints([0, 0]), ints([0, 0]), o[:0], lse[:0], workspace=prompt_ws(a))
+    cd = ispa.kvq_desc(1, 64, 16, 1, ispa.ISPA_KVQ_INT8)
+    kvq = torch.full((ispa.ispa_kvq_bytes(cd),), 9, dtype=torch.uint8, device="cuda")
+    ispa.ispa_kvq_write(cd, none, none, ints([[0]]), ints([0]), ints([0, 0]), kvq)
+    ispa.ispa_kvq_read(cd, kvq, ints([[0]]), ints([0, 0]), none, none)
+    assert torch.all(kvq == 9)
+    ispa.ispa_check_device_error()
+
+
+def test_cached_attention_scales_far_apart():
+    """V rows over 2^24 of scale: each keeps its share, whichever comes first."""
+    rng = np.random.default_rng(63)
+    for order in (1, -1):
+        k = rand16(rng, (200, 1, 64), torch.bfloat16)
+        v = (rand16(rng, (200, 1, 64), torch.bfloat16).float() * torch.exp2(torch.linspace(-12.0 * order, 12.0 * order, 200))[:, None, None]).to(torch.bfloat16)
+        q = rand16(rng, (1, 4, 64), torch.bfloat16)
+        for fmt in FMT:
+            cd = ispa.kvq_desc(1, 64, 16, 13, FMT[fmt])
+            c = so.Cache(fmt, 1, 64, 16, 13)
+            c.put(np.arange(13), np.arange(200), f64(k), f64(v))
+            a = ispa.attn_seq_desc(1, 4, 1, 64, ispa.ISPA_BF16, ispa.ISPA_F32)
+            o = torch.empty(1, 4, 64, device="cuda")
+            ispa.ispa_attn_kvq(a, cd, q.cuda(), cuda(c.buf), ints([np.arange(13)]), ints([200]), ints([0, 1]), o, None, workspace=attn_ws(a, cd))
+            kk, vv = c.get(np.arange(13), np.arange(200))
+            # weights below 2^-14 of fp16's unit are off by 2^-25: at most 2^-31 of the largest V scale times its largest code
+            check_attention(o, None, so.attention(f64(q), kk, vv, True), 2.0 ** -11, 64, 200, np.abs(vv).max())
     ispa.ispa_check_device_error()
 
 
