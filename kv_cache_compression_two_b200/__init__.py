@@ -404,26 +404,25 @@ def ispa_selftest_wait_timeout(wait_ns: int, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # A decoding step's calls take a few microseconds on the device, so their checks
 # are kept to a few attribute reads a tensor; _explain says what was wrong.
-_seq_env = None
+# (What they need of torch is looked up by the first of them.)
+_I32 = _U8 = _F32 = _CODES = _current_device = _raw_stream = None
 
 
-def _seq():
-    """(int32, uint8, float32, dtype codes, current device, raw current stream of a device), looked up once."""
-    global _seq_env
-    if _seq_env is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
-        _seq_env = (torch.int32, torch.uint8, torch.float32,
-                    {torch.bfloat16: ISPA_BF16, torch.float16: ISPA_F16, torch.float32: ISPA_F32},
-                    torch.cuda.current_device, raw)
-    return _seq_env
+def _seq_init() -> None:
+    global _I32, _U8, _F32, _CODES, _current_device, _raw_stream
+    import torch
+    _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
+    _CODES = {torch.bfloat16: ISPA_BF16, torch.float16: ISPA_F16, torch.float32: ISPA_F32}
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _explain(x, name, want, shape, dev) -> Exception:
     import torch
     if not isinstance(x, torch.Tensor):
         return TypeError(f"{name}: expected a torch.Tensor")
-    if x.get_device() != dev or dev != _seq()[4]():
+    if x.get_device() != dev:
         return ValueError(f"{name}: on {x.device}; every tensor of a call must be on the current device")
     return ValueError(f"{name}: {x.dtype} {tuple(x.shape)}, strides {x.stride()}; expected {want} {shape}")
 
@@ -442,7 +441,7 @@ def _rows(x, name, heads, d, code, dev):
     """Packed rows [T, heads, d] whose tokens may be strided: (address, T, stride)."""
     try:
         T, h, c = x.shape
-        if h == heads and c == d and _seq()[3].get(x.dtype, -1) == code != ISPA_F32 and x.get_device() == dev:
+        if h == heads and c == d and _CODES.get(x.dtype, -1) == code != ISPA_F32 and x.get_device() == dev:
             st, sh, sc = x.stride()
             if T <= 1:
                 st = heads * d
@@ -459,26 +458,27 @@ def _device(x, name) -> int:
         dev = x.get_device()
     except AttributeError:
         raise TypeError(f"{name}: expected a torch.Tensor") from None
-    if dev < 0 or dev != _seq()[4]():
+    if _raw_stream is None:
+        _seq_init()
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"{name}: on {x.device}; every tensor of a call must be on the current device")
     return dev
 
 
 def _cache(desc, kvq, table, B, dev):
     """Addresses of the cache and its block table, and the table's width."""
-    env = _seq()
-    need = lib().ispa_kvq_bytes(desc)
+    need = _lib.ispa_kvq_bytes(desc)
     if need == 0:
         raise ValueError("desc: not a valid cache layout")
     n = kvq.numel()
     if n < need:
         raise ValueError(f"kvq: {n} bytes, the layout needs {need}")
     wide = table.shape[-1]
-    return _flat(kvq, "kvq", env[1], (n,), dev), _flat(table, "block_table", env[0], (B, wide), dev), wide
+    return _flat(kvq, "kvq", _U8, (n,), dev), _flat(table, "block_table", _I32, (B, wide), dev), wide
 
 
 def _at(stream, dev):
-    return _seq()[5](dev) if stream is None else _stream(stream)
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def ispa_kvq_bytes(desc: KvqDesc) -> int:
@@ -487,29 +487,29 @@ def ispa_kvq_bytes(desc: KvqDesc) -> int:
 
 def ispa_kvq_write(desc: KvqDesc, k, v, block_table, seq_lens, cu_new, kvq, stream=None) -> None:
     """Quantises the packed rows k, v [T, H_kv, d] into the cache (seq_lens counts them already)."""
-    dev, i32 = _device(k, "k"), _seq()[0]
-    code = _seq()[3].get(k.dtype, -1)
+    dev = _device(k, "k")
+    code = _CODES.get(k.dtype, -1)
     B = seq_lens.shape[0]
     kp, T, ks = _rows(k, "k", desc.H_kv, desc.head_dim, code, dev)
     vp, Tv, vs = _rows(v, "v", desc.H_kv, desc.head_dim, code, dev)
     if T != Tv:
         raise ValueError(f"k has {T} rows, v {Tv}")
     cp, tp, wide = _cache(desc, kvq, block_table, B, dev)
-    _check(lib().ispa_kvq_write(desc, B, T, tp, wide, _flat(seq_lens, "seq_lens", i32, (B,), dev),
-                                _flat(cu_new, "cu_new", i32, (B + 1,), dev), kp, ks, vp, vs, code, cp,
-                                _at(stream, dev)))
+    _check(_lib.ispa_kvq_write(desc, B, T, tp, wide, _flat(seq_lens, "seq_lens", _I32, (B,), dev),
+                               _flat(cu_new, "cu_new", _I32, (B + 1,), dev), kp, ks, vp, vs, code, cp,
+                               _at(stream, dev)))
 
 
 def ispa_kvq_read(desc: KvqDesc, kvq, block_table, cu_out, k_out, v_out, seq_begin=None, stream=None) -> None:
     """Reads positions seq_begin[b] + i of each sequence back into the packed k_out, v_out [T, H_kv, d]."""
-    dev, i32 = _device(kvq, "kvq"), _seq()[0]
+    dev = _device(kvq, "kvq")
     B, T = cu_out.shape[0] - 1, k_out.shape[0]
     shape, dtype = (T, desc.H_kv, desc.head_dim), k_out.dtype
     cp, tp, wide = _cache(desc, kvq, block_table, B, dev)
-    begin = None if seq_begin is None else _flat(seq_begin, "seq_begin", i32, (B,), dev)
-    _check(lib().ispa_kvq_read(desc, B, T, tp, wide, begin, _flat(cu_out, "cu_out", i32, (B + 1,), dev), cp,
-                               _flat(k_out, "k_out", dtype, shape, dev), _flat(v_out, "v_out", dtype, shape, dev),
-                               _seq()[3].get(dtype, -1), _at(stream, dev)))
+    begin = None if seq_begin is None else _flat(seq_begin, "seq_begin", _I32, (B,), dev)
+    _check(_lib.ispa_kvq_read(desc, B, T, tp, wide, begin, _flat(cu_out, "cu_out", _I32, (B + 1,), dev), cp,
+                              _flat(k_out, "k_out", dtype, shape, dev), _flat(v_out, "v_out", dtype, shape, dev),
+                              _CODES.get(dtype, -1), _at(stream, dev)))
 
 
 def ispa_attn_kvq_workspace_bytes(desc: AttnSeqDesc, cache: KvqDesc) -> int:
@@ -518,27 +518,26 @@ def ispa_attn_kvq_workspace_bytes(desc: AttnSeqDesc, cache: KvqDesc) -> int:
 
 def _outputs(desc, T, o, lse, workspace, dev):
     """Addresses of o, lse and the workspace, and the workspace's size."""
-    env = _seq()
     shape = (T, desc.H, desc.head_dim)
-    if env[3].get(getattr(o, "dtype", None), -1) != desc.out_dtype:
+    if _CODES.get(getattr(o, "dtype", None), -1) != desc.out_dtype:
         raise _explain(o, "o", f"ISPA dtype {desc.out_dtype}", shape, dev)
     if workspace is None:
         raise ValueError("workspace: required")
     n = workspace.numel()
-    return (_flat(o, "o", o.dtype, shape, dev), None if lse is None else _flat(lse, "lse", env[2], shape[:2], dev),
-            _flat(workspace, "workspace", env[1], (n,), dev), n)
+    return (_flat(o, "o", o.dtype, shape, dev), None if lse is None else _flat(lse, "lse", _F32, shape[:2], dev),
+            _flat(workspace, "workspace", _U8, (n,), dev), n)
 
 
 def ispa_attn_kvq(desc: AttnSeqDesc, cache: KvqDesc, q, kvq, block_table, seq_lens, cu_q, o, lse=None, workspace=None,
                   stream=None) -> None:
     """Attention of the packed queries q [T, H, d] over each sequence's quantised cache."""
-    dev, i32, B = _device(q, "q"), _seq()[0], desc.B
+    dev, B = _device(q, "q"), desc.B
     qp, T, qs = _rows(q, "q", desc.H, desc.head_dim, desc.in_dtype, dev)
     cp, tp, wide = _cache(cache, kvq, block_table, B, dev)
     op, lp, wp, wn = _outputs(desc, T, o, lse, workspace, dev)
-    _check(lib().ispa_attn_kvq(desc, cache, T, _flat(cu_q, "cu_q", i32, (B + 1,), dev), tp, wide,
-                               _flat(seq_lens, "seq_lens", i32, (B,), dev), qp, qs, cp, op, lp, wp, wn,
-                               _at(stream, dev)))
+    _check(_lib.ispa_attn_kvq(desc, cache, T, _flat(cu_q, "cu_q", _I32, (B + 1,), dev), tp, wide,
+                              _flat(seq_lens, "seq_lens", _I32, (B,), dev), qp, qs, cp, op, lp, wp, wn,
+                              _at(stream, dev)))
 
 
 def ispa_attn_prompt_workspace_bytes(desc: AttnSeqDesc) -> int:
@@ -547,16 +546,16 @@ def ispa_attn_prompt_workspace_bytes(desc: AttnSeqDesc) -> int:
 
 def ispa_attn_prompt(desc: AttnSeqDesc, q, k, v, cu_q, cu_k, o, lse=None, workspace=None, stream=None) -> None:
     """Attention of packed prompts: q [Tq, H, d] over k, v [Tk, H_kv, d]."""
-    dev, i32, B = _device(q, "q"), _seq()[0], desc.B
+    dev, B = _device(q, "q"), desc.B
     qp, Tq, qs = _rows(q, "q", desc.H, desc.head_dim, desc.in_dtype, dev)
     kp, Tk, ks = _rows(k, "k", desc.H_kv, desc.head_dim, desc.in_dtype, dev)
     vp, Tv, vs = _rows(v, "v", desc.H_kv, desc.head_dim, desc.in_dtype, dev)
     if Tk != Tv:
         raise ValueError(f"k has {Tk} rows, v {Tv}")
     op, lp, wp, wn = _outputs(desc, Tq, o, lse, workspace, dev)
-    _check(lib().ispa_attn_prompt(desc, Tq, Tk, _flat(cu_q, "cu_q", i32, (B + 1,), dev),
-                                  _flat(cu_k, "cu_k", i32, (B + 1,), dev), qp, qs, kp, ks, vp, vs, op, lp, wp, wn,
-                                  _at(stream, dev)))
+    _check(_lib.ispa_attn_prompt(desc, Tq, Tk, _flat(cu_q, "cu_q", _I32, (B + 1,), dev),
+                                 _flat(cu_k, "cu_k", _I32, (B + 1,), dev), qp, qs, kp, ks, vp, vs, op, lp, wp, wn,
+                                 _at(stream, dev)))
 
 
 lib()
