@@ -777,6 +777,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
 }
 
 // Joins the parts of the item that slot 2c + 1 starts (c = blockIdx.x).
+// (A launch of its own, made ahead and waiting on the device: joining in the attention's kernel, by
+// the last of an item's CTAs to arrive at a counter, took 12.6 us instead of 10.2 for one sequence
+// of 999 tokens and 27 instead of 23.4 for 16 sequences with pending tokens.)
 template <int D, int NR, typename TO>
 __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   constexpr int kRows = 8 * NR;
@@ -792,8 +795,8 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   if (n == 0) return;
   const PartMeta own = P.meta[2 * c + 1];
   const int h = own.head, n_rows = own.count;
-  // kItems threads take a row's eight columns each; with fewer rows, several threads take
-  // every kSplit-th part of the same columns and are added up in shared memory
+  // a thread takes a row's eight columns; with fewer rows, several threads take every split-th
+  // part of the same columns and are added up in shared memory
   __shared__ float red[256][11];
   const int items = n_rows * (D / 8);
   int split = 1;
