@@ -404,14 +404,13 @@ def ispa_selftest_wait_timeout(wait_ns: int, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # A decoding step's calls take a few microseconds on the device, so their checks
 # are kept to a few attribute reads a tensor; _explain says what was wrong.
-# (The first of them loads the library and looks up what they need of torch.)
+# (What they need of torch is looked up by the first of them.)
 _I32 = _U8 = _F32 = _CODES = _current_device = _raw_stream = None
 
 
 def _seq_init() -> None:
     global _I32, _U8, _F32, _CODES, _current_device, _raw_stream
     import torch
-    lib()
     _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
     _CODES = {torch.bfloat16: ISPA_BF16, torch.float16: ISPA_F16, torch.float32: ISPA_F32}
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device

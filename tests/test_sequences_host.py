@@ -3,8 +3,6 @@ import ctypes
 import math
 import os
 import re
-import subprocess
-import sys
 
 import numpy as np
 import pytest
@@ -206,16 +204,3 @@ def test_attention_oracle_against_loops():
     assert np.all(o[:2] == 0) and np.all(np.isneginf(lse[:2])) and np.allclose(o[2, 0], v[0, 0])
     o, lse, _, _ = so.attention(q, k[:0], v[:0], False)
     assert np.all(o == 0) and np.all(np.isneginf(lse))
-
-
-def test_first_sequence_call_loads_the_library():
-    # in a process of its own: nothing before the call has loaded it
-    code = ("import kv_cache_compression_two_b200 as K\n"
-            "import torch\n"
-            "assert K._lib is None\n"
-            "try:\n"
-            "    K.ispa_attn_prompt(K.attn_seq_desc(1, 1, 1, 64, 1, 1), torch.zeros(1, 1, 64), None, None, None, None, None)\n"
-            "except ValueError as e:\n"
-            "    assert 'current device' in str(e), e\n"
-            "assert K._lib is not None\n")
-    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
