@@ -465,15 +465,22 @@ def _device(x, name) -> int:
     return dev
 
 
+def _numel(x, name) -> int:
+    try:
+        return x.numel()
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
+
+
 def _cache(desc, kvq, table, B, dev):
     """Addresses of the cache and its block table, and the table's width."""
     need = _lib.ispa_kvq_bytes(desc)
     if need == 0:
         raise ValueError("desc: not a valid cache layout")
-    n = kvq.numel()
+    n = _numel(kvq, "kvq")
     if n < need:
         raise ValueError(f"kvq: {n} bytes, the layout needs {need}")
-    wide = table.shape[-1]
+    wide = _numel(table, "block_table") // max(B, 1)
     return _flat(kvq, "kvq", _U8, (n,), dev), _flat(table, "block_table", _I32, (B, wide), dev), wide
 
 
@@ -489,7 +496,7 @@ def ispa_kvq_write(desc: KvqDesc, k, v, block_table, seq_lens, cu_new, kvq, stre
     """Quantises the packed rows k, v [T, H_kv, d] into the cache (seq_lens counts them already)."""
     dev = _device(k, "k")
     code = _CODES.get(k.dtype, -1)
-    B = seq_lens.shape[0]
+    B = _numel(seq_lens, "seq_lens")
     kp, T, ks = _rows(k, "k", desc.H_kv, desc.head_dim, code, dev)
     vp, Tv, vs = _rows(v, "v", desc.H_kv, desc.head_dim, code, dev)
     if T != Tv:
@@ -503,9 +510,10 @@ def ispa_kvq_write(desc: KvqDesc, k, v, block_table, seq_lens, cu_new, kvq, stre
 def ispa_kvq_read(desc: KvqDesc, kvq, block_table, cu_out, k_out, v_out, seq_begin=None, stream=None) -> None:
     """Reads positions seq_begin[b] + i of each sequence back into the packed k_out, v_out [T, H_kv, d]."""
     dev = _device(kvq, "kvq")
-    B, T = cu_out.shape[0] - 1, k_out.shape[0]
-    shape, dtype = (T, desc.H_kv, desc.head_dim), k_out.dtype
+    B = _numel(cu_out, "cu_out") - 1
     cp, tp, wide = _cache(desc, kvq, block_table, B, dev)
+    T = _numel(k_out, "k_out") // (desc.H_kv * desc.head_dim)
+    shape, dtype = (T, desc.H_kv, desc.head_dim), k_out.dtype
     begin = None if seq_begin is None else _flat(seq_begin, "seq_begin", _I32, (B,), dev)
     _check(_lib.ispa_kvq_read(desc, B, T, tp, wide, begin, _flat(cu_out, "cu_out", _I32, (B + 1,), dev), cp,
                               _flat(k_out, "k_out", dtype, shape, dev), _flat(v_out, "v_out", dtype, shape, dev),
@@ -523,7 +531,7 @@ def _outputs(desc, T, o, lse, workspace, dev):
         raise _explain(o, "o", f"ISPA dtype {desc.out_dtype}", shape, dev)
     if workspace is None:
         raise ValueError("workspace: required")
-    n = workspace.numel()
+    n = _numel(workspace, "workspace")
     return (_flat(o, "o", o.dtype, shape, dev), None if lse is None else _flat(lse, "lse", _F32, shape[:2], dev),
             _flat(workspace, "workspace", _U8, (n,), dev), n)
 

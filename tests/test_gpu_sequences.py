@@ -647,3 +647,23 @@ def test_binding_refuses_what_does_not_fit():
             ispa.ispa_attn_kvq(a, cd, q, kvq, table, lens, ints([0, 1]), kw.get("o", torch.empty_like(q)), None,
                                workspace=kw["workspace"])
     torch.cuda.synchronize()
+
+
+def test_binding_names_an_argument_that_is_no_tensor():
+    cd = ispa.kvq_desc(2, 64, 16, 4, ispa.ISPA_KVQ_INT8)
+    kvq = torch.zeros(ispa.ispa_kvq_bytes(cd), dtype=torch.uint8, device="cuda")
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    table, lens, cu = ints([[0, 1]]), ints([3]), ints([0, 3])
+    names = ("k", "v", "block_table", "seq_lens", "cu_new", "kvq")
+    for i, name in enumerate(names):
+        args = [k, k, table, lens, cu, kvq]
+        args[i] = [1, 2, 3]
+        with pytest.raises(TypeError, match=name):
+            ispa.ispa_kvq_write(cd, *args)
+    names = ("kvq", "block_table", "cu_out", "k_out", "v_out", "seq_begin")
+    for i, name in enumerate(names):
+        args = [kvq, table, cu, torch.empty_like(k), torch.empty_like(k), lens]
+        args[i] = [1, 2, 3]
+        with pytest.raises(TypeError, match=name):
+            ispa.ispa_kvq_read(cd, *args)
+    torch.cuda.synchronize()

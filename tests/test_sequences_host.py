@@ -204,3 +204,21 @@ def test_attention_oracle_against_loops():
     assert np.all(o[:2] == 0) and np.all(np.isneginf(lse[:2])) and np.allclose(o[2, 0], v[0, 0])
     o, lse, _, _ = so.attention(q, k[:0], v[:0], False)
     assert np.all(o == 0) and np.all(np.isneginf(lse))
+
+
+def test_binding_names_an_argument_that_is_no_tensor():
+    torch = pytest.importorskip("torch")
+    ispa._seq_init()
+    d = cache()
+    buf = torch.zeros(ispa.ispa_kvq_bytes(d), dtype=torch.uint8)
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    assert ispa._cache(d, buf, table, 2, -1) == (buf.data_ptr(), table.data_ptr(), 3)
+    for kvq, tab, name in ((None, table, "kvq"), (buf, [[0]], "block_table")):
+        with pytest.raises(TypeError, match=name):
+            ispa._cache(d, kvq, tab, 2, -1)
+    with pytest.raises(ValueError, match="block_table"):
+        ispa._cache(d, buf, table.view(-1), 2, -1)
+    with pytest.raises(ValueError, match="block_table"):
+        ispa._cache(d, buf, table, 3, -1)
+    with pytest.raises(TypeError, match="workspace"):
+        ispa._outputs(attn(), 1, torch.zeros(1, 8, 128, dtype=torch.bfloat16), None, 4096, -1)
