@@ -18,12 +18,12 @@
 // CTAs hold are merged by kvq_merge_kernel.  Three or four CTAs share an SM, so that
 // an item's start and end in one are covered by the others: 48 sequences of 200 to
 // 16000 tokens took 137 us with one CTA of 12 warps an SM and items counted by their
-// tiles, 78 us with four warps and an item's fixed cost counted.
+// tiles, 78 us (71 now) with four warps and an item's fixed cost counted.
 //
-// Measured: those 48 sequences (406 MB, e4m3, 8 heads of 128, groups of 4) 72.5 us,
-// 5.6 TB/s, 0.86 of the measured copy rate; 102960 tokens of 40 heads in int4 (593 MB)
+// Measured: those 48 sequences (406 MB, e4m3, 8 heads of 128, groups of 4) 71 us,
+// 5.7 TB/s, 0.87 of the measured copy rate; 102960 tokens of 40 heads in int4 (593 MB)
 // 143 us, 4.1 TB/s, 0.64, bound by the integer pipe and issue slots (760 instructions
-// a 32-token tile, of which 160 unpack nibbles); one sequence of 999 tokens 10.5 us.
+// a 32-token tile, of which 160 unpack nibbles); one sequence of 999 tokens 10.2 us.
 //
 // Codes go into fp16 exactly: e4m3 and int8 values as they are, int4 values
 // times the group's e4m3 factor (7 significant bits).  The per-token scales
@@ -776,32 +776,60 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
   }
 }
 
-// Joins the parts of the item that slot 2c + 1 starts (c = blockIdx.x).
+// Who joins which columns of a cut item.  CTA c takes the item that its slot 2c + 1 starts; when
+// that has many parts, the CTAs c + 1 .. c + shares - 1, whose slots the item runs through, take
+// equal shares of its values: two from 16 parts on, four from 32 (shares <= parts / 8, so that a
+// helper never is the item's last CTA).  4 sequences of 30000 tokens of one head, 150 parts each: 34
+// -> 24 us, 16 with pending tokens: 23.2 -> 22.1 (512 threads a CTA instead: 27 and 23.4; sharing from
+// 8 parts on: 0.5 us more for one sequence of 999 tokens; up to eight CTAs: no gain).
+constexpr int kMaxShares = 4, kShareParts = 16;
+struct MergeRole {
+  int head, share, shares, n;  // n: the item's parts, 0: nothing to do
+};
+__device__ __forceinline__ MergeRole merge_role(const PartMeta *meta, int nc, int c) {  // by a whole warp
+  const int lane = threadIdx.x & 31, at = c - lane;
+  const bool see = lane < kMaxShares && at >= 0;
+  const int through = see ? *const_cast<const volatile int *>(&meta[2 * at].state) : 0;
+  const int starts = see ? *const_cast<const volatile int *>(&meta[2 * at + 1].state) : 0;
+  const unsigned heads = __ballot_sync(0xffffffffu, starts != 0), runs = __ballot_sync(0xffffffffu, through == 1);
+  MergeRole m = {0, 0, 1, 0};
+  if (heads == 0) return m;
+  m.share = __ffs(heads) - 1;
+  const unsigned below = (1u << m.share) - 1;
+  if ((runs & below) != below) return m;  // (the item ended before c)
+  m.head = c - m.share;
+  const int n = parts_from(meta, nc, m.head);
+  while (m.shares < kMaxShares && n >= kShareParts * m.shares) m.shares *= 2;
+  m.n = m.share < m.shares ? n : 0;
+  return m;
+}
+
+// Joins the parts of the cut items.
 // (A launch of its own, made ahead and waiting on the device: joining in the attention's kernel, by
 // the last of an item's CTAs to arrive at a counter, took 12.6 us instead of 10.2 for one sequence
-// of 999 tokens and 27 instead of 23.4 for 16 sequences with pending tokens.)
+// of 999 tokens and 27 instead of 23.2 for 16 sequences with pending tokens.)
 template <int D, int NR, typename TO>
 __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
   constexpr int kRows = 8 * NR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x;
-  __shared__ int s_n;
+  __shared__ MergeRole role;
   if (threadIdx.x < 32) {
-    const int n = part_count(P.meta, P.nc, c);
-    if (threadIdx.x == 0) s_n = n;
+    const MergeRole m = merge_role(P.meta, P.nc, blockIdx.x);
+    if (threadIdx.x == 0) role = m;
   }
   __syncthreads();
-  const int n = s_n;
+  const int n = role.n, c = role.head;
   if (n == 0) return;
   const PartMeta own = P.meta[2 * c + 1];
   const int h = own.head, n_rows = own.count;
   // a thread takes a row's eight columns; with fewer rows, several threads take every split-th
   // part of the same columns and are added up in shared memory
   __shared__ float red[256][11];
-  const int items = n_rows * (D / 8);
+  const int all = n_rows * (D / 8);
+  const int first = all * role.share / role.shares, items = all * (role.share + 1) / role.shares;
   int split = 1;
-  while (split * 2 * items <= 256 && split < n) split *= 2;
-  for (int i0 = 0; i0 < items; i0 += 256 / split) {
+  while (split * 2 * (items - first) <= 256 && split < n) split *= 2;
+  for (int i0 = first; i0 < items; i0 += 256 / split) {
     const int i = i0 + threadIdx.x / split, sub = threadIdx.x % split;
     const int r = i / (D / 8), c8 = i % (D / 8) * 8;
     float mm = kNegInf, ll = 0.f, x[8] = {};

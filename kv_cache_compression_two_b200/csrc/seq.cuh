@@ -179,10 +179,10 @@ struct __align__(16) PartMeta {
 
 // A stretch's first CTA owns an item that slot 2c + 1 starts; its parts are
 // that slot and slots 2c' of the CTAs behind it up to the first with state 2.
-// Returns their number (0: nothing to merge); part i > 0 is in slot 2 (c + i).
+// part_count returns their number (0: nothing to merge), parts_from the same when
+// an item is known to start there; part i > 0 is in slot 2 (c + i).
 // Called by a whole warp: 32 states are read at a time.
-__device__ __forceinline__ int part_count(const PartMeta *meta, int nc, int c) {
-  if (*const_cast<const volatile int *>(&meta[2 * c + 1].state) == 0) return 0;
+__device__ __forceinline__ int parts_from(const PartMeta *meta, int nc, int c) {
   const int lane = threadIdx.x & 31;
   for (int n = 1; c + n < nc; n += 32) {
     const int at = c + n + lane;
@@ -194,6 +194,10 @@ __device__ __forceinline__ int part_count(const PartMeta *meta, int nc, int c) {
     }
   }
   return nc - c;
+}
+
+__device__ __forceinline__ int part_count(const PartMeta *meta, int nc, int c) {
+  return *const_cast<const volatile int *>(&meta[2 * c + 1].state) == 0 ? 0 : parts_from(meta, nc, c);
 }
 
 __device__ __forceinline__ int part_slot(int c, int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); }

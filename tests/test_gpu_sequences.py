@@ -183,6 +183,14 @@ def test_cached_attention_split_over_sms(fmt):
     run_attn_kvq(np.random.default_rng(8), fmt, 128, "bf16", torch.float32, 4, 1, 64, [1, 5], [9001, 4097])
 
 
+@pytest.mark.parametrize("fmt,d,dtype,G", [("int8", 64, "bf16", 1), ("e4m3", 128, "fp16", 3), ("int4", 64, "fp16", 13)])
+def test_cached_attention_from_few_to_many_parts(fmt, d, dtype, G):
+    """Items of about 6, 18, 36 and 70 parts, whose merge one, two or four CTAs share; one alone of 150."""
+    rng = np.random.default_rng([12, d])
+    run_attn_kvq(rng, fmt, d, dtype, torch.float32, G, 1, 32, [1] * 4, [700, 2300, 4600, 9000])
+    run_attn_kvq(rng, fmt, d, dtype, torch.float32, G, 1, 256, [2], [19001])
+
+
 @pytest.mark.parametrize("fmt,d", [("e4m3", 128), ("int8", 64), ("int4", 128)])
 def test_cached_attention_wide_scales(fmt, d):
     """Token scales over ten powers of two, and a sharp softmax."""
