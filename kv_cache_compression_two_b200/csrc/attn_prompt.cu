@@ -37,10 +37,10 @@
 // the FMA pipe (the same to 10 % slower), one thread a row with the scores in registers
 // (spills), spinning waits, one pass over the scores with a late correction (spills).
 //
-// Measured (bf16, d = 128): 8192 causal tokens, 32 heads on 8, 455 us, 1210 TFLOP/s (0.72
+// Measured (bf16, d = 128): 8192 causal tokens, 32 heads on 8, 450 us, 1220 TFLOP/s (0.72
 // of the measured burst peak, 0.86 of the sustained one); 4680 queries over 32760 keys, 12
-// heads, 742 us alone, 1270 TFLOP/s; six prompts of 545 to 2815 tokens 164 us, 850
-// TFLOP/s; 24 prompts of 1 to 300 tokens (d = 64) 14.3 us.
+// heads, 742 us alone, 1270 TFLOP/s; six prompts of 545 to 2815 tokens 157 us, 890
+// TFLOP/s; 24 prompts of 1 to 300 tokens (d = 64) 14.1 us.
 //
 // Ordering (MMAs of one thread execute in order; a commit fires when all
 // earlier ones have completed): S_{j+1} is issued after PV_j of the same tile,

@@ -2,12 +2,12 @@
 //
 // Both are one pass over their bytes.  Reading is bound by memory: 184 MB (23400 tokens
 // of 12 heads, int4) in 38 us, 4.9 TB/s, 0.75 of the measured copy rate (it writes four
-// bytes for each one read).  Writing is bound by its arithmetic, about 27 instructions
-// a lane and value with the reductions: 14 us for 4680 tokens of 12 heads (37 MB, 2.6 TB/s;
-// 25 us with a division a value).  A decoding step's few rows are bound by the launch.  A row (one token of one head) is handled
-// by d / 16 lanes, 16 values each: with 8 a lane the reductions and reciprocals of
-// a row cost as much as its values.  A warp takes one token
-// and up to kHeads heads of K and of V, whose loads are all issued before the
+// bytes for each one read).  Writing is bound by its arithmetic, about 20 instructions
+// a lane and value with the reductions: 12 us for 4680 tokens of 12 heads (37 MB, 3.1 TB/s;
+// 25 us with a division a value).  A decoding step's few rows are bound by the launch.
+// A row (one token of one head) is handled by d / 16 lanes, 16 values each: with 8 a
+// lane the reductions and reciprocals of a row cost as much as its values.  A warp takes
+// one token and up to kHeads heads of K and of V, whose loads are all issued before the
 // first is used.
 //
 // The codes are those of real arithmetic, ties included, without a division an
