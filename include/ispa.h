@@ -659,9 +659,11 @@ typedef struct {
  *        key gives O = 0, lse = -inf.
  *   Arithmetic: q in fp16 scaled by a power of two per row (exact for entries
  *   above 2^-29 of the row's largest), codes exactly in fp16, products
- *   accumulated in fp32; softmax statistics in fp32; the weights, times the
- *   V scale, enter the second product in fp16 (11 significant bits; for fp16
- *   inputs as the sum of two fp16 numbers).
+ *   accumulated in fp32; softmax statistics in fp32; each weight times its
+ *   token's V scale enters the second product in fp16 (for fp16 inputs as the
+ *   sum of two fp16 numbers), relative to the query's own largest such product:
+ *   11 significant bits down to 2^-23 of that, below it an error of at most
+ *   2^-34 of it.  Tokens that a query does not see do not enter.
  *   workspace >= ispa_attn_kvq_workspace_bytes(...), 16-byte aligned: partial
  *   results of sequences that several SMs share.  Calls (or captured graphs)
  *   that may run at the same time need one each.  The same inputs give the

@@ -28,8 +28,11 @@
 // Codes go into fp16 exactly: e4m3 and int8 values as they are, int4 values
 // times the group's e4m3 factor (7 significant bits).  The per-token scales
 // are applied outside the products: K's to the scores in fp32, V's to the
-// softmax weights before they are rounded to fp16 (relative to the largest V
-// scale seen, as a power of two, so that the weights stay in fp16's range).
+// softmax weights before they are rounded to fp16.  A weight times its V scale
+// enters the product times a power of two of its row, which puts the largest such
+// product among the row's own visible keys so far between 2^9 and 2^15: keys that a row
+// does not see, or gives no weight, do not move it, however large their V.  A weight is
+// then off by at most 2^-34 of the row's largest product where fp16 has no 11 bits left.
 // Channels are assigned to operand positions so that each lane's bytes of a
 // row are contiguous: Q is permuted to match, and O comes out in runs of d/8.
 #include <algorithm>
@@ -50,7 +53,12 @@ constexpr int kMaxCtas = 4;       // CTAs per SM at most (Geo::CTAS)
 constexpr int kItem = 8;          // steps counted for an item besides its tiles
 constexpr int kMinTail = 4;       // tiles that are worth cutting off
 constexpr int kMinHead = kItem + kMinTail;
-constexpr float kRescale = 8.f;   // the reference maximum moves when passed by more than this (log2)
+constexpr float kAhead = 4.f;     // a row's reference is put this far (log2) above its largest score, and moves
+                                  // when a score passes it by as much: weights are at most 2^4, so that their
+                                  // products with V's scales (below 2^121) stay in fp32's range
+constexpr int kUpMax = 253;       // exponent field of a row's power of two at most (2^126)
+constexpr int kUpTo = 127 + 9;    // its largest product is put into [2^9, 2^10) ...
+constexpr float kUpLimit = 32768.f;  // ... and moved when it comes to this
 constexpr float kNegInf = -INFINITY;
 
 struct KvqParams {
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
       for (int nr = 0; nr < NR; ++nr) qb[ks][nr] = reinterpret_cast<const uint2 *>(qh)[(ks * NR + nr) * 32 + lane];
     // this lane's rows: 8 nr + 2 t4 + e; the keys that each may see
     const int past = len - rows.n + 1;
-    float un[NR][2], m[NR][2], l[NR][2];
+    float un[NR][2], m[NR][2], l[NR][2], up[NR][2];
     int lim[NR][2];
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
@@ -445,10 +453,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
         lim[nr][e] = P.causal ? min(len, past + (rb * kRows + r) / P.G) : len;
         m[nr][e] = kNegInf;
         l[nr][e] = 0.f;
+        up[nr][e] = __uint_as_float((uint32_t)kUpMax << 23);
       }
     const int lim_all = P.causal ? min(len, past + (rb * kRows) / P.G) : len;  // the first row sees the fewest
 
-    int ve = -200;  // exponent of the largest V scale so far: weights enter the product times 2^(6 - ve)
     float acc[Ge::MB][NR][4];
 #pragma unroll
     for (int j = 0; j < Ge::MB; ++j)
@@ -565,62 +573,97 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
           }
       }
 
-      // ---- the running maximum and V scale move only when some lane's tokens pass them
+      // ---- the running maximum moves only when some lane's tokens pass it
       float mx[NR][2];
-      const float vmx = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-      bool move = (int)(__float_as_uint(vmx) >> 23) - 127 > ve;
+      bool move = false;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mx[nr][e] = fmaxf(fmaxf(s[0][nr][e], s[0][nr][2 + e]), fmaxf(s[1][nr][e], s[1][nr][2 + e])) * un[nr][e];
-          move |= mx[nr][e] > m[nr][e] + kRescale;
+          move |= mx[nr][e] > m[nr][e] + kAhead;
         }
       if (__any_sync(0xffffffffu, move)) {
-        float v = vmx;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) mx[nr][e] = fmaxf(mx[nr][e], __shfl_xor_sync(0xffffffffu, mx[nr][e], o));
-        }
-        const int nv = max(ve, (int)(__float_as_uint(v) >> 23) - 127);  // floor(log2), -127 for zeros
-        const float fv = ve == -200 ? 0.f : exp2_fast((float)(ve - nv));
-        ve = nv;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float to = mx[nr][e] > m[nr][e] ? mx[nr][e] : m[nr][e];
+            const float to = fmaxf(m[nr][e], mx[nr][e] + kAhead);
             const float f = m[nr][e] == kNegInf ? 0.f : exp2_fast(m[nr][e] - to);
             m[nr][e] = to;
             l[nr][e] *= f;
+            // the earlier products shrink by f: the power of two grows by as much, so that small V scales
+            // among the keys that now matter keep their bits
+            const int was = (int)(__float_as_uint(up[nr][e]) >> 23);
+            const int now = min(was + 127 - (int)(__float_as_uint(f) >> 23), kUpMax);
+            up[nr][e] = __uint_as_float((uint32_t)now << 23);
+            const float g = f * __uint_as_float((uint32_t)(127 + now - was) << 23);
 #pragma unroll
             for (int j = 0; j < Ge::MB; ++j) {
-              acc[j][nr][e] *= f * fv;
-              acc[j][nr][2 + e] *= f * fv;
+              acc[j][nr][e] *= g;
+              acc[j][nr][2 + e] *= g;
             }
           }
       }
 
-      // ---- weights: exp2, times V's scale, to fp16, transposed
-      const float vup = __uint_as_float((uint32_t)(min(127 + 6 - ve, 254)) << 23);  // 2^(6 - ve)
+      // ---- weights: exp2, times V's scale
+      bool over = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float ref = m[nr][e] == kNegInf ? 0.f : m[nr][e];
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float &w = s[k >> 1][nr][2 * (k & 1) + e];
+            const float p = exp2_fast(fmaf(w, un[nr][e], -ref));
+            l[nr][e] += p;
+            w = p * vs[k >> 1][k & 1];
+            top = fmaxf(top, w);
+          }
+          mx[nr][e] = top;
+          over |= top * up[nr][e] >= kUpLimit;
+        }
+      if (__any_sync(0xffffffffu, over)) {  // the first tile, and where a row's products grow 32-fold
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mx[nr][e] = fmaxf(mx[nr][e], __shfl_xor_sync(0xffffffffu, mx[nr][e], o));
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (mx[nr][e] * up[nr][e] >= kUpLimit) {
+              const int was = (int)(__float_as_uint(up[nr][e]) >> 23);
+              const int now = min(127 + kUpTo - (int)(__float_as_uint(mx[nr][e]) >> 23), kUpMax);
+              up[nr][e] = __uint_as_float((uint32_t)now << 23);
+              const float g = __uint_as_float((uint32_t)max(127 + now - was, 0) << 23);
+#pragma unroll
+              for (int j = 0; j < Ge::MB; ++j) {
+                acc[j][nr][e] *= g;
+                acc[j][nr][2 + e] *= g;
+              }
+            }
+      }
+
+      // ---- to fp16, transposed
       uint2 pb[2][NR], pl[2][NR];
 #pragma unroll
       for (int tb = 0; tb < 2; ++tb) {
-        const float va = vs[tb][0] * vup, vb = vs[tb][1] * vup;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           float w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float ref = m[nr][i & 1] == kNegInf ? 0.f : m[nr][i & 1];
-            const float p = exp2_fast(fmaf(s[tb][nr][i], un[nr][i & 1], -ref));
-            l[nr][i & 1] += p;
-            w[i] = p * (i < 2 ? va : vb);
-          }
+          for (int i = 0; i < 4; ++i) w[i] = s[tb][nr][i] * up[nr][i & 1];
           const uint32_t h0 = pack_half2(w[0], w[1]), h1 = pack_half2(w[2], w[3]);
           pb[tb][nr] = make_uint2(transpose8(h0), transpose8(h1));
           if (kTwoParts) {
@@ -712,12 +755,12 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
     float *mg = reinterpret_cast<float *>(smem);  // [warp][m | l | O rows x D]
     {
       float *mine = mg + warp * kRows * (D + 2);
-      const float vdown = ve == -200 ? 0.f : __uint_as_float((uint32_t)(max(127 + ve - 6, 0)) << 23);
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = nr * 8 + 2 * t4 + e;
+          const float down = __uint_as_float((254u << 23) - __float_as_uint(up[nr][e]));  // 1 / up, exactly
           if (g == 0) {
             mine[r] = m[nr][e];
             mine[kRows + r] = l[nr][e];
@@ -725,8 +768,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
           float4 *oo = reinterpret_cast<float4 *>(mine + 2 * kRows + r * D + g * (D / 8));
 #pragma unroll
           for (int j = 0; j < Ge::MB; j += 2)
-            oo[j / 2] = make_float4(acc[j][nr][e] * vdown, acc[j][nr][2 + e] * vdown, acc[j + 1][nr][e] * vdown,
-                                    acc[j + 1][nr][2 + e] * vdown);
+            oo[j / 2] = make_float4(acc[j][nr][e] * down, acc[j][nr][2 + e] * down, acc[j + 1][nr][e] * down,
+                                    acc[j + 1][nr][2 + e] * down);
         }
     }
     __syncthreads();
