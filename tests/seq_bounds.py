@@ -71,6 +71,9 @@ def run_cached(rng, fmt, q, k, v, lens, new, out=torch.float32, causal=True, pag
     return o, lse
 
 
-def random_rows(rng, T, lens, H, H_kv, d, dtype):
-    q = rand16(rng, (T, H, d), dtype)
-    return (q, *(rand16(rng, (sum(lens), H_kv, d), dtype) for _ in range(2)))
+def random_rows(rng, T, lens, H, H_kv, d, dtype, slope=0.0):
+    """q, k, v; slope: V's mean runs from -slope to slope over each sequence, so that every stretch of it shows in O."""
+    q, k, v = (rand16(rng, (n, h, d), dtype) for n, h in ((T, H), (sum(lens), H_kv), (sum(lens), H_kv)))
+    if slope:
+        v = (v.float() + torch.cat([torch.linspace(-slope, slope, n) for n in lens])[:, None, None]).to(dtype)
+    return q, k, v

@@ -1,0 +1,42 @@
+"""GPU tests of the cached attention where items are cut and joined, against a bound that a lost part does not pass."""
+import numpy as np
+import pytest
+import torch
+
+from seq_bounds import random_rows, run_cached
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8", "int4"])
+def test_items_cut_by_many_sms(fmt):
+    rng = np.random.default_rng(8)
+    lens, new = [9001, 4097], [1, 5]
+    run_cached(rng, fmt, *random_rows(rng, 6, lens, 4, 1, 128, torch.bfloat16, 4.0), lens, new, page=64)
+
+
+@pytest.mark.parametrize("fmt,d,dtype,G", [("int8", 64, torch.bfloat16, 1), ("e4m3", 128, torch.float16, 3),
+                                           ("int4", 64, torch.float16, 13), ("int4", 128, torch.bfloat16, 2)])
+def test_items_joined_by_one_two_or_four_ctas(fmt, d, dtype, G):
+    """Items of about 6, 18, 36 and 70 parts, and one alone of 150."""
+    rng = np.random.default_rng([12, d])
+    for lens, new, page in (([700, 2300, 4600, 9000], [1] * 4, 32), ([19001], [2], 256)):
+        run_cached(rng, fmt, *random_rows(rng, sum(new), lens, G, 1, d, dtype, 4.0), lens, new, page=page)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8", "int4"])
+@pytest.mark.parametrize("d,dtype,out,G,H_kv,page", [
+    (128, torch.bfloat16, torch.bfloat16, 4, 2, 16), (64, torch.float16, torch.float16, 7, 3, 32),
+    (128, torch.float16, torch.float32, 1, 5, 64), (64, torch.bfloat16, torch.float32, 16, 1, 256)])
+def test_one_token(fmt, d, dtype, out, G, H_kv, page):
+    rng = np.random.default_rng([d, G])
+    lens = [1, 15, 16, 17, 31, 32, 33, 300, 1025, 2]
+    run_cached(rng, fmt, *random_rows(rng, 10, lens, G * H_kv, H_kv, d, dtype), lens, [1] * 10, out, page=page)
+
+
+@pytest.mark.parametrize("fmt,d", [("e4m3", 64), ("int8", 128), ("int4", 128), ("int4", 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_several_tokens(fmt, d, causal):
+    rng = np.random.default_rng(d)
+    lens, new = [2, 50, 200, 0, 700, 1, 64], [2, 0, 7, 1, 16, 3, 40]
+    run_cached(rng, fmt, *random_rows(rng, sum(new), lens, 6, 2, d, torch.bfloat16), lens, new, causal=causal, page=16)
