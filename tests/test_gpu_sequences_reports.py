@@ -1,0 +1,57 @@
+"""GPU tests of the sequence calls' reports: bounds out of range are named, and touch nothing that they do not own."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_compression_two_b200 as ispa
+from oracle import seq_oracle as so
+from seq_bounds import ints
+from seq_helpers import check_attention, f64, rand16
+
+pytestmark = pytest.mark.gpu
+
+
+def reported():
+    """The sequence in the error word (cleared by this), or None.  (No exception is kept: see the older tests.)"""
+    try:
+        ispa.ispa_check_device_error()
+    except ispa.IspaError as e:
+        assert e.status == ispa.ISPA_ERR_INVALID_ARG
+        return int(str(e).split("sequence ")[1].split()[0])
+    return None
+
+
+# ------------------------------------------------------------------ prompts
+@pytest.mark.parametrize("cu_q,cu_k,bad", [([0, 30, 30, 50], [0, 30, 9999, 9999], (1, 2)), ([0, 30, 70, 70], [0, 30, 35, 40], (1, 2)),
+                                           ([0, 30, 35, 20], [0, 30, 35, 40], (2,)), ([-3, 30, 35, 40], [0, 30, 35, 40], (0,)),
+                                           ([0, 30, 35, 40], [0, 30, 35, -1], (2,)), ([0, 30, 35, 40], [0, 30, 35, 40], None)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_name_a_bad_bound(cu_q, cu_k, bad, causal):
+    rng = np.random.default_rng(52)
+    k, v = (rand16(rng, (40, 1, 64), torch.bfloat16) for _ in range(2))
+    q = rand16(rng, (40, 2, 64), torch.bfloat16)
+    a = ispa.attn_seq_desc(3, 2, 1, 64, ispa.ISPA_BF16, ispa.ISPA_F32, causal)
+    ws = torch.empty(ispa.ispa_attn_prompt_workspace_bytes(a), dtype=torch.uint8, device="cuda")
+    o = torch.empty(40, 2, 64, device="cuda")
+    assert reported() is None
+    ispa.ispa_attn_prompt(a, q.cuda(), k.cuda(), v.cuda(), ints(cu_q), ints(cu_k), o, None, workspace=ws)
+    got = reported()
+    assert got in bad if bad else got is None
+    if cu_q[0] == 0 and (not bad or 0 not in bad) and cu_q[3] != 20:  # (a later sequence that overlaps writes there too)
+        check_attention(o[:30], None, so.attention(f64(q[:30]), f64(k[:30]), f64(v[:30]), causal), 2.0 ** -8, 64, 30, 5.0)
+
+
+@pytest.mark.parametrize("lens,cu,bad", [([30, -7, 30], [0, 1, 2, 3], (1,)), ([30, 30, 5], [0, 1, 2, 900], (2,)),
+                                         ([30, 30, 30], [0, 1, 2, -4], (2,)), ([30, 33, 30], [0, 1, 2, 3], (1,)),
+                                         ([30, 30, 30], [0, 1, 2, 3], None)])
+def test_cached_attention_names_a_bad_bound(lens, cu, bad):
+    rng = np.random.default_rng(53)
+    cd = ispa.kvq_desc(1, 64, 16, 6, ispa.ISPA_KVQ_INT8)
+    kvq = torch.zeros(ispa.ispa_kvq_bytes(cd), dtype=torch.uint8, device="cuda")
+    a = ispa.attn_seq_desc(3, 2, 1, 64, ispa.ISPA_BF16, ispa.ISPA_F32)
+    ws = torch.empty(ispa.ispa_attn_kvq_workspace_bytes(a, cd), dtype=torch.uint8, device="cuda")
+    q, o = rand16(rng, (3, 2, 64), torch.bfloat16).cuda(), torch.empty(3, 2, 64, device="cuda")
+    assert reported() is None
+    ispa.ispa_attn_kvq(a, cd, q, kvq, ints([[0, 1], [2, 3], [4, 5]]), ints(lens), ints(cu), o, None, workspace=ws)
+    got = reported()
+    assert got in bad if bad else got is None
