@@ -43,7 +43,8 @@ __device__ __forceinline__ int seq_len(const int *lens, int b, int cap) {
 
 // The sequence that owns packed row t, or -1; executed by a whole warp with a
 // uniform t.  Each round narrows the candidates 32-fold by a ballot, so that
-// 1024 sequences cost two dependent loads.
+// 1024 sequences cost two dependent loads.  (The last check holds for every t
+// unless bounds decrease: the search may then end at a sequence without the row.)
 __device__ __forceinline__ int seq_of_row(const int *cu, int B, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = B;  // the first b in [lo, lo + n) with cu[b + 1] > t
@@ -58,7 +59,7 @@ __device__ __forceinline__ int seq_of_row(const int *cu, int B, int t) {
     n = min(step, n - skip);
     if (step == 1) break;
   }
-  return n > 0 && lo < B && __ldg(cu + lo) <= t ? lo : -1;
+  return n > 0 && lo < B && __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
 }
 
 // a b / n and a / b; in 32 bits where they fit (64-bit division is a long routine, and these

@@ -55,3 +55,17 @@ def test_cached_attention_names_a_bad_bound(lens, cu, bad):
     ispa.ispa_attn_kvq(a, cd, q, kvq, ints([[0, 1], [2, 3], [4, 5]]), ints(lens), ints(cu), o, None, workspace=ws)
     got = reported()
     assert got in bad if bad else got is None
+
+
+# ------------------------------------------------------------------ the cache
+def test_decreasing_bounds_write_nothing_past_a_sequence():
+    """Rows 2..7 lie in no sequence, but a search that takes the bounds as ascending ends at the last one."""
+    k = rand16(np.random.default_rng(56), (8, 1, 64), torch.bfloat16).cuda()
+    cd = ispa.kvq_desc(1, 64, 16, 3, ispa.ISPA_KVQ_INT8)
+    c = so.Cache("int8", 1, 64, 16, 3, fill=0xAB)
+    kvq = torch.as_tensor(c.buf.copy()).cuda()
+    ispa.ispa_kvq_write(cd, k, k, ints([[0], [1], [2]]), ints([8, 8, 8]), ints([0, 8, 1, 2]), kvq)
+    reported()
+    c.buf[:] = kvq.cpu().numpy()
+    for which in range(4):
+        assert np.all(c.parts[which][:, :, 8:] == 0xAB)
