@@ -140,12 +140,22 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], uint4 &code, ui
   }
 }
 
+// The last block of a launch has no rows: it looks over every sequence's bounds, those
+// that no row falls in among them, beside the rows' way and not in front of it.
+__device__ __forceinline__ bool bounds_block(const RowParams &P) {
+  if (blockIdx.x + 1 != gridDim.x) return false;
+  for (int b = threadIdx.x; b < P.B; b += kThreads)
+    if (seq_rows_bad(P.cu, b, P.T)) report_seq(P.err, b);
+  return true;
+}
+
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads) kvq_write_kernel(RowParams P) {
   constexpr int W = D / 16;                       // lanes of a row
   constexpr int kRows = 32 / W;                   // rows of a pass: K and V of kStep heads
   constexpr int kHeads = 4, kStep = kRows / 2;    // heads of a warp, heads of a pass
   constexpr int ROW = FMT == ISPA_KVQ_INT4 ? D / 2 : D, REC = FMT == ISPA_KVQ_INT4 ? 8 : 4;
+  if (bounds_block(P)) return;
   const int lane = threadIdx.x & 31;
   const int h_parts = (P.H_kv + kHeads - 1) / kHeads;
   const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -167,9 +177,9 @@ __global__ void __launch_bounds__(kThreads) kvq_write_kernel(RowParams P) {
   const int c0 = __ldg(P.cu + b), c1 = __ldg(P.cu + b + 1);
   const long long pos = (long long)__ldg(P.lens + b) - (c1 - c0) + (t - c0);
   const int page = P.c.page(b, pos);
-  if (page < 0 || seq_rows_bad(P.cu, b, P.T)) {
+  if (page < 0) {
     if (lane == 0) report_seq(P.err, b);
-    if (page < 0) return;
+    return;
   }
   const int place = (int)(pos & ((1 << P.c.page_log2) - 1));
   unsigned char *codes = is_v ? P.c.v_code : P.c.k_code, *scales = is_v ? P.c.v_scale : P.c.k_scale;
@@ -215,6 +225,7 @@ __global__ void __launch_bounds__(kThreads) kvq_read_kernel(RowParams P) {
   constexpr int kRows = 32 / W;
   constexpr int kHeads = 4, kStep = kRows / 2, kN = kHeads / kStep;
   constexpr int ROW = FMT == ISPA_KVQ_INT4 ? D / 2 : D, REC = FMT == ISPA_KVQ_INT4 ? 8 : 4;
+  if (bounds_block(P)) return;
   const int lane = threadIdx.x & 31;
   const int h_parts = (P.H_kv + kHeads - 1) / kHeads;
   const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) kvq_read_kernel(RowParams P) {
   if (b < 0) return;
   const long long pos = (long long)(P.begin ? __ldg(P.begin + b) : 0) + (t - __ldg(P.cu + b));
   const int page = P.c.page(b, pos);
-  if ((page < 0 || seq_rows_bad(P.cu, b, P.T)) && lane == 0) report_seq(P.err, b);
+  if (page < 0 && lane == 0) report_seq(P.err, b);
   const int place = (int)(pos & ((1 << P.c.page_log2) - 1));
   const int sub = lane / W, l = lane % W;
   const bool is_v = sub >= kStep;
@@ -305,7 +316,7 @@ ispa_status launch_kvq(const ispa_kvq_desc &d, RowParams P, bool write, ispa_dty
   if (st != ISPA_OK) return st;
   P.err = e.word;
   const long long items = (long long)P.T * ((d.H_kv + 3) / 4);
-  const unsigned grid = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned grid = (unsigned)((items + kThreads / 32 - 1) / (kThreads / 32)) + 1;  // (and bounds_block)
   if (d.fmt == ISPA_KVQ_E4M3)
     launch_rows_fmt<ISPA_KVQ_E4M3>(P, write, d.head_dim, dt, grid, s);
   else if (d.fmt == ISPA_KVQ_INT8)

@@ -69,3 +69,70 @@ def test_decreasing_bounds_write_nothing_past_a_sequence():
     c.buf[:] = kvq.cpu().numpy()
     for which in range(4):
         assert np.all(c.parts[which][:, :, 8:] == 0xAB)
+
+
+BAD_BOUNDS = [([0, 4, 4, 9], (2,)), ([0, 4, 8, 3], (2,)), ([0, 8, 1, 2], (1,)), ([-2, 4, 6, 8], (0,)), ([9, 9, 9, 9], (0, 1, 2)),
+              ([0, 8, 8, -1], (2,)), ([0, 5, 3, 8], (1,)), ([0, 4, 6, 8], None), ([0, 0, 0, 0], None), ([2, 3, 3, 7], None)]
+
+
+def rows_of(cu, T):
+    """Rows that each sequence may own (its bounds clamped to the tensor)."""
+    return [range(min(max(a, 0), T), min(max(b, 0), T)) for a, b in zip(cu, cu[1:])]
+
+
+@pytest.mark.parametrize("cu,bad", BAD_BOUNDS)
+def test_writing_names_a_bad_bound_and_stays_inside_the_sequences(cu, bad):
+    """Sequences that own no row are looked at too; a position past a sequence's length is never written."""
+    rng = np.random.default_rng(54)
+    T, page, lens = 8, 16, [10, 9, 8]
+    cd = ispa.kvq_desc(1, 64, page, 8, ispa.ISPA_KVQ_INT8)
+    c = so.Cache("int8", 1, 64, page, 8, fill=0xAB)
+    kvq, k = torch.as_tensor(c.buf.copy()).cuda(), rand16(rng, (T, 1, 64), torch.bfloat16).cuda()
+    table = np.asarray([[3, 7], [5, 0], [6, 1]])
+    assert reported() is None
+    ispa.ispa_kvq_write(cd, k, k, ints(table), ints(lens), ints(cu), kvq)
+    got = reported()
+    assert got in bad if bad else got is None
+    c.buf[:] = kvq.cpu().numpy()
+    for b, n in enumerate(lens):
+        for which in range(4):
+            assert np.all(c.parts[which][table[b, 0], :, n:] == 0xAB) and np.all(c.parts[which][table[b, 1]] == 0xAB)
+    if not bad:
+        for b, rows in enumerate(rows_of(cu, T)):
+            pos = np.arange(lens[b] - len(rows), lens[b])
+            want = so.quantise("int8", f64(k[rows.start:rows.stop]))[0]
+            assert np.array_equal(c.parts[0][table[b, 0], :, pos].reshape(-1, 64), want.reshape(-1, 64))
+
+
+@pytest.mark.parametrize("cu,bad", BAD_BOUNDS)
+def test_reading_names_a_bad_bound(cu, bad):
+    rng = np.random.default_rng(55)
+    T, page = 8, 16
+    cd = ispa.kvq_desc(1, 64, page, 8, ispa.ISPA_KVQ_E4M3)
+    c = so.Cache("e4m3", 1, 64, page, 8)
+    table = np.asarray([[3, 7], [5, 0], [6, 1]])
+    for b in range(3):
+        c.put(table[b], np.arange(32), *(f64(rand16(rng, (32, 1, 64), torch.bfloat16)) for _ in range(2)))
+    out = [torch.full((T, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert reported() is None
+    ispa.ispa_kvq_read(cd, torch.as_tensor(c.buf).cuda(), ints(table), ints(cu), *out)
+    got = reported()
+    assert got in bad if bad else got is None
+    if not bad:
+        owned = np.zeros(T, bool)
+        for b, rows in enumerate(rows_of(cu, T)):
+            owned[rows.start:rows.stop] = True
+            for x, want in zip(out, c.get(table[b], np.arange(len(rows)))):
+                assert torch.equal(x[rows.start:rows.stop].cpu(), torch.from_numpy(want).to(torch.bfloat16))
+        assert torch.all(out[0][torch.from_numpy(~owned).cuda()] == 7.0)
+
+
+def test_reading_names_a_position_without_a_page():
+    cd = ispa.kvq_desc(1, 64, 16, 4, ispa.ISPA_KVQ_INT4)
+    kvq = torch.zeros(ispa.ispa_kvq_bytes(cd), dtype=torch.uint8, device="cuda")
+    for begin, bad in (([0, 31, 0], 1), ([0, 0, -1], 2), ([30, 30, 30], None)):
+        out = [torch.full((6, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        assert reported() is None
+        ispa.ispa_kvq_read(cd, kvq, ints([[0, 1], [1, 2], [2, 3]]), ints([0, 2, 4, 6]), *out, seq_begin=ints(begin))
+        assert reported() == bad
+        assert torch.all(out[0] == 0) and torch.all(out[1] == 0)
