@@ -686,7 +686,9 @@ ispa_status ispa_attn_kvq(const ispa_attn_seq_desc *desc, const ispa_kvq_desc *c
  *   o    [Tq, H, d] out_dtype, lse [Tq, H] fp32 or NULL.  A query that sees no
  *        key gives O = 0, lse = -inf.
  *   tcgen05 tensor cores, fp32 accumulation and statistics; the softmax
- *   weights enter the second product in in_dtype.
+ *   weights enter the second product in in_dtype: bf16 with 8 significant bits;
+ *   fp16 with 11 down to 2^-21 of the query's largest, below it with an error of
+ *   at most 2^-32 of that.
  *   workspace >= ispa_attn_prompt_workspace_bytes(desc), as for ispa_attn_kvq.
  */
 size_t ispa_attn_prompt_workspace_bytes(const ispa_attn_seq_desc *desc);

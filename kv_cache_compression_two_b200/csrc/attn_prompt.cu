@@ -72,7 +72,18 @@ constexpr int kItem = 2;         // steps counted for an item besides its own: f
 constexpr int kMinPart = 6;      // steps that are worth cutting off
 constexpr int kSegs = 4;         // items handed on ahead
 constexpr int kSegReaders = 18;  // producer, issuer, sixteen softmax warps
-constexpr float kThreshold = 8.0f;  // the reference maximum moves when passed by more than this (log2)
+// A row's reference lies `behind` below its largest score (log2) and moves when one passes it by
+// more than `limit`, so that weights are at most 2^limit.  bf16 has fp32's range.  fp16 weights use
+// what theirs has upwards (2^15), and the small ones of a long row keep their bits: a weight is
+// off by at most 2^-25 where fp16's normal numbers end, 2^-32 of the row's largest.
+template <typename T>
+struct Ref {
+  static constexpr float behind = 0.f, limit = 8.f;
+};
+template <>
+struct Ref<__half> {
+  static constexpr float behind = 7.f, limit = 15.f;
+};
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct PromptParams {
@@ -717,9 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         mt = fmaxf(mt, *theirs) * P.scale_log2;
         if (j == j0) {
-          m_ref = mt == -INFINITY ? 0.f : mt;
-        } else if (__any_sync(0xffffffffu, mt > m_ref + kThreshold)) {
-          const float m_new = fmaxf(m_ref, mt);
+          m_ref = mt == -INFINITY ? 0.f : mt - Ref<T>::behind;
+        } else if (__any_sync(0xffffffffu, mt > m_ref + Ref<T>::limit)) {
+          const float m_new = fmaxf(m_ref, mt - Ref<T>::behind);
           const float f = exp2_fast(m_ref - m_new);
           m_ref = m_new;
           l *= f;
@@ -733,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(col_o + c, o);
           }
         }
-        // P = 2^(s scale log2e - m_ref) <= 2^8 in the input type, over the first 64 columns of S
+        // P = 2^(s scale log2e - m_ref) in the input type, over the first 64 columns of S
         const float2 sc2 = make_float2(P.scale_log2, P.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import kv_cache_compression_two_b200 as ispa
-from seq_bounds import FMT, random_rows, run_cached
+from oracle import seq_oracle as so
+from seq_bounds import FMT, ints, random_rows, run_cached
+from seq_helpers import check_attention, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +94,29 @@ def test_values_at_the_ends_of_the_type(fmt):
     o, _ = run_cached(rng, fmt, q, k, (v.float() * 2.0 ** -80).to(torch.bfloat16), [100], [1])
     want, _ = run_cached(rng, fmt, q, k, v, [100], [1])
     assert torch.allclose(o * 2.0 ** 80, want, rtol=2.0 ** -9, atol=2.0 ** -14)
+
+
+# ------------------------------------------------------------------ prompts: small weights of fp16
+@pytest.mark.parametrize("d,first,n,nq", [(64, True, 6000, 3), (128, False, 6000, 300), (128, True, 700, 40), (64, False, 40, 1)])
+@pytest.mark.parametrize("log2", [-18, -26])
+@pytest.mark.parametrize("causal", [True, False])
+def test_small_weights_of_a_prompt_add_up(d, first, n, nq, log2, causal):
+    """One key holds nearly all of the weight and no value; many of weight 2^log2 hold the output.
+
+    A weight is off by 2^-11 of itself or by 2^-25 in units in which the row's largest is at least
+    2^7: 2^-32 max|v| a key."""
+    rng = np.random.default_rng([n, d, -log2])
+    q, k, v = random_rows(rng, nq, [n], 2, 1, d, torch.float16)
+    base = torch.randn(d, generator=torch.Generator().manual_seed(3))
+    q = base.expand(nq, 2, d).to(torch.float16)
+    k = (0.02 * k.float() + log2 * np.log(2.0) * d ** 0.5 / float(base @ base) * base).to(torch.float16)
+    v = v.float().abs().add(0.5).to(torch.float16)
+    one = 0 if first else n - nq
+    k[one], v[one] = 0, 0
+    a = ispa.attn_seq_desc(1, 2, 1, d, ispa.ISPA_F16, ispa.ISPA_F32, causal)
+    o, lse = torch.empty(nq, 2, d, device="cuda"), torch.empty(nq, 2, device="cuda")
+    ws = torch.empty(ispa.ispa_attn_prompt_workspace_bytes(a), dtype=torch.uint8, device="cuda")
+    ispa.ispa_attn_prompt(a, q.cuda(), k.cuda(), v.cuda(), ints([0, nq]), ints([0, n]), o, lse, workspace=ws)
+    ispa.ispa_check_device_error()
+    ref = so.attention(f64(q), f64(k), f64(v), causal)
+    check_attention(o, lse, ref, 2.0 ** -11, d, n, f64(v).max() * 2.0 ** -7)
