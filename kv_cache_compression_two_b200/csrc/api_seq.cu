@@ -52,7 +52,7 @@ ispa_status check_attn(const ispa_attn_seq_desc *d, float *scale) {
   if (d->out_dtype != d->in_dtype && d->out_dtype != ISPA_F32)
     return fail(ISPA_ERR_INVALID_ARG, "out_dtype must be in_dtype or ISPA_F32");
   if (d->causal != 0 && d->causal != 1) return fail(ISPA_ERR_INVALID_ARG, "causal must be 0 or 1");
-  *scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.f / sqrtf((float)d->head_dim);
+  *scale = d->softmax_scale <= 0.f ? 1.f / sqrtf((float)d->head_dim) : d->softmax_scale;
   if (!isfinite(*scale)) return fail(ISPA_ERR_INVALID_ARG, "softmax_scale must be finite");
   return ISPA_OK;
 }
