@@ -656,7 +656,8 @@ typedef struct {
  * tokens is taken; the cache is read once per 8 rows of tokens * (H / H_kv) when
  * there are no more than 8 to a sequence on the average, else once per 16.
  *   o    [T, H, d] out_dtype, lse [T, H] fp32 or NULL.  A query that sees no
- *        key gives O = 0, lse = -inf.
+ *        key gives O = 0, lse = -inf; one that holds a NaN gives NaN in its own
+ *        rows of both.
  *   Arithmetic: q in fp16 scaled by a power of two per row (exact for entries
  *   above 2^-29 of the row's largest), codes exactly in fp16, products
  *   accumulated in fp32; softmax statistics in fp32; each weight times its
@@ -681,10 +682,11 @@ ispa_status ispa_attn_kvq(const ispa_attn_seq_desc *desc, const ispa_kvq_desc *c
  * [cu_k[b], cu_k[b+1]) of k and v [Tk, H_kv, d].  With fewer queries than keys
  * the queries are the last ones (a chunk after a prefix, e.g. one brought back
  * by ispa_kvq_read); with causal and more queries than keys the first queries
- * see nothing.  The rows of one sequence must hold finite values; those of
+ * see nothing.  The keys and values of one sequence must be finite; those of
  * others, and padding, do not matter to it.
  *   o    [Tq, H, d] out_dtype, lse [Tq, H] fp32 or NULL.  A query that sees no
- *        key gives O = 0, lse = -inf.
+ *        key gives O = 0, lse = -inf; one that holds a NaN gives NaN in its own
+ *        rows of both.
  *   tcgen05 tensor cores, fp32 accumulation and statistics; the softmax
  *   weights enter the second product in in_dtype: bf16 with 8 significant bits;
  *   fp16 with 11 down to 2^-21 of the query's largest, below it with an error of

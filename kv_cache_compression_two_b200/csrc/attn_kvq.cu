@@ -796,11 +796,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
       if (whole) {
         const int rr = rb * kRows + r;
         const long long out = (long long)(rows.begin + rr / P.G) * P.H + h * P.G + rr % P.G;
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a sum that is NaN stays so)
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] *= inv;
         store8(static_cast<TO *>(P.o) + out * D + c8, x);
-        if (P.lse && c8 == 0) P.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : kNegInf;
+        if (P.lse && c8 == 0) P.lse[out] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * 0.69314718055994530942f;
       } else {
         if (c8 == 0) {
           part[r] = mm;
@@ -912,11 +912,11 @@ __global__ void __launch_bounds__(256) kvq_merge_kernel(KvqParams P) {
     if (i >= items || sub != 0) continue;
     const int rr = own.first + r;
     const long long out = (long long)(own.row + rr / P.G) * P.H + h * P.G + rr % P.G;
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a sum that is NaN stays so)
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] *= inv;
     store8(static_cast<TO *>(P.o) + out * D + c8, x);
-    if (P.lse && c8 == 0) P.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : kNegInf;
+    if (P.lse && c8 == 0) P.lse[out] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * 0.69314718055994530942f;
   }
 }
 

@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = swap_sync();  // read before the next item's first maximum takes its place
         if (!ok) break;
       }
-      const bool some = l > 0.f;
+      const bool some = l != 0.f;  // (a sum that is NaN stays so)
       if (mode == 1) {
         const float inv = some ? 1.f / l : 0.f;
         const long long out = (long long)out_row * P.H + out_head;
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kTile) prompt_merge_kernel(PromptParams P) {
     }
   }
   const long long out = (long long)(own.row + t) * P.H + own.head * P.G + head;
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a sum that is NaN stays so)
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     float y[8];
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kTile) prompt_merge_kernel(PromptParams P) {
     for (int t = 0; t < 8; ++t) y[t] = x[8 * v + t] * inv;
     store8(static_cast<TO *>(P.o) + out * D + c0 + v * 8, y);
   }
-  if (P.lse && c0 == 0) P.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+  if (P.lse && c0 == 0) P.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
 }
 
 template <int D, typename T, typename TO>
