@@ -432,7 +432,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, NR>::THREADS, Geo<FMT, D, NR>::CTA
         reinterpret_cast<__half *>(qh)[(((ks * NR + (r >> 3)) * 32 + (r & 7) * 4 + t) * 2 + half) * 2 + el] =
             __float2half_rn(x[i] * up);
       }
-      if (lane == 0) q_unscale[r] = P.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+      // (never 0, which would make NaN of a masked score: the scores that it scales are below 2^128, so that
+      // 2^-149 leaves them as good as 0 too)
+      if (lane == 0) q_unscale[r] = fmaxf(P.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 0x1p-149f);
     }
     __syncthreads();
     uint2 qb[Ge::KS][NR];

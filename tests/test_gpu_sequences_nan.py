@@ -74,3 +74,27 @@ def test_nan_queries_of_prompts(d, dtype, causal):
     ispa.ispa_attn_prompt(a, poisoned(q), k.cuda(), v.cuda(), ints([0, 5, 8]), ints([0, 100, 3100]), o, lse, workspace=ws)
     ispa.ispa_check_device_error()
     outputs_are_nan_where_queries_are(o, lse, refs, HALF[dtype], d, f64(v).max() * 2.0 ** -7)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_a_scale_times_a_query_below_every_fp32_number(fmt):
+    """Scores as good as 0: the mean of the values, with tokens masked in the last tile."""
+    rng = np.random.default_rng(73)
+    q, k, v = random_rows(rng, 2, [50], 2, 1, 64, torch.bfloat16)
+    tiny = (q.float() * 2.0 ** -126).to(torch.bfloat16)
+    c = so.Cache(fmt, 1, 64, 64, 1)
+    c.put([0], np.arange(50), f64(k), f64(v))
+    kk, vv = c.get([0], np.arange(50))
+    cd = ispa.kvq_desc(1, 64, 64, 1, FMT[fmt])
+    a = ispa.attn_seq_desc(1, 2, 1, 64, ispa.ISPA_BF16, ispa.ISPA_F32, True, 2.0 ** -30)
+    o, lse = torch.empty(2, 2, 64, device="cuda"), torch.empty(2, 2, device="cuda")
+    ws = torch.empty(ispa.ispa_attn_kvq_workspace_bytes(a, cd), dtype=torch.uint8, device="cuda")
+    ispa.ispa_attn_kvq(a, cd, tiny.cuda(), torch.as_tensor(c.buf).cuda(), ints([[0]]), ints([50]), ints([0, 2]), o, lse,
+                       workspace=ws)
+    ispa.ispa_check_device_error()
+    check_attention(o, lse, so.attention(f64(tiny), kk, vv, True, 2.0 ** -30), 2.0 ** -11, 64, 50, np.abs(vv).max() * 2.0 ** -9)
+    ap = ispa.attn_seq_desc(1, 2, 1, 64, ispa.ISPA_BF16, ispa.ISPA_F32, True, 2.0 ** -30)
+    wp = torch.empty(ispa.ispa_attn_prompt_workspace_bytes(ap), dtype=torch.uint8, device="cuda")
+    ispa.ispa_attn_prompt(ap, tiny.cuda(), k.cuda(), v.cuda(), ints([0, 2]), ints([0, 50]), o, lse, workspace=wp)
+    ispa.ispa_check_device_error()
+    check_attention(o, lse, so.attention(f64(tiny), f64(k), f64(v), True, 2.0 ** -30), 2.0 ** -8, 64, 50, 5.0)
