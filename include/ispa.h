@@ -654,7 +654,8 @@ typedef struct {
  * [T, H, d], its keys the first seq_lens[b] tokens of its cache; with causal,
  * the queries are its last tokens (already written).  Any number of query
  * tokens is taken; the cache is read once per 8 rows of tokens * (H / H_kv) when
- * there are no more than 8 to a sequence on the average, else once per 16.
+ * the call has no more than 16 to a sequence on the average (T * (H / H_kv) / B,
+ * rows of padding counted), else once per 16.
  *   o    [T, H, d] out_dtype, lse [T, H] fp32 or NULL.  A query that sees no
  *        key gives O = 0, lse = -inf; one that holds a NaN gives NaN in its own
  *        rows of both.
@@ -665,6 +666,8 @@ typedef struct {
  *   sum of two fp16 numbers), relative to the query's own largest such product:
  *   11 significant bits down to 2^-23 of that, below it an error of at most
  *   2^-34 of it.  Tokens that a query does not see do not enter.
+ *   Scores and sums are fp32 numbers: K rows with values above 2^100 and V rows
+ *   above 2^90 can pass their range.
  *   workspace >= ispa_attn_kvq_workspace_bytes(...), 16-byte aligned: partial
  *   results of sequences that several SMs share.  Calls (or captured graphs)
  *   that may run at the same time need one each.  The same inputs give the

@@ -950,11 +950,20 @@ ispa_status launch_rows(KvqParams P, cudaStream_t s) {
   return cuda_status(e, "kvq_merge launch");
 }
 
-// Row blocks of 8 when a sequence's rows fit one (on the average: the arrays are on the device),
-// else of 16, which read the cache half as often.
+// Row blocks of 8 up to 16 rows a sequence, else of 16, which read and unpack the cache half as
+// often.  The number is an average over the call, rows of padding counted (the arrays are on the
+// device), and the two sides lie close together around it: 16 sequences of 3000 to 9000 tokens, 4 K/V
+// heads, us with blocks of 8 / of 16:
+//   rows a sequence      8            9            16           32
+//   e4m3, d = 128    28.2 / 36.2  34.0 / 38.6  34.8 / 38.6  53.2 / 50.3
+//   int8, d = 128    29.9 / 38.2  38.9 / 39.9  39.6 / 40.3  63.1 / 54.6
+//   int4, d = 128    29.0 / 35.8  39.6 / 37.9  40.1 / 38.1  62.3 / 53.2
+//   e4m3, d = 64     23.0 / 26.5  26.6 / 27.5  27.3 / 27.1  40.5 / 35.2
+// (With the line at 8, one row of padding took a batch of 8 rows a sequence from the left column
+// to its right side.)
 template <int FMT, int D, typename T, typename TO>
 ispa_status launch_one(const KvqParams &P, cudaStream_t s) {
-  return (long long)P.G * P.T <= 8LL * P.B ? launch_rows<FMT, D, 1, T, TO>(P, s) : launch_rows<FMT, D, 2, T, TO>(P, s);
+  return (long long)P.G * P.T <= 16LL * P.B ? launch_rows<FMT, D, 1, T, TO>(P, s) : launch_rows<FMT, D, 2, T, TO>(P, s);
 }
 
 template <int FMT, int D>

@@ -40,3 +40,16 @@ def test_several_tokens(fmt, d, causal):
     rng = np.random.default_rng(d)
     lens, new = [2, 50, 200, 0, 700, 1, 64], [2, 0, 7, 1, 16, 3, 40]
     run_cached(rng, fmt, *random_rows(rng, sum(new), lens, 6, 2, d, torch.bfloat16), lens, new, causal=causal, page=16)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8", "int4"])
+@pytest.mark.parametrize("d,G", [(128, 8), (64, 8), (128, 5)])
+def test_a_few_rows_of_padding_change_no_bit(fmt, d, G):
+    """A batch of up to 8 rows a sequence takes the same kernel with padding behind it."""
+    rng = np.random.default_rng([91, d])
+    lens = [int(n) for n in rng.integers(1, 900, 8)]
+    q, k, v = random_rows(rng, 8, lens, G, 1, d, torch.bfloat16)
+    o, lse = run_cached(np.random.default_rng(0), fmt, q, k, v, lens, [1] * 8)
+    more = torch.cat([q, torch.full((3, G, d), float("nan"), dtype=q.dtype)])
+    o2, lse2 = run_cached(np.random.default_rng(0), fmt, more, k, v, lens, [1] * 8)
+    assert torch.equal(o, o2[:8]) and torch.equal(lse, lse2[:8]) and torch.all(o2[8:] == 7.0) and torch.all(lse2[8:] == 7.0)
