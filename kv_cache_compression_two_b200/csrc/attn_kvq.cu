@@ -22,8 +22,14 @@
 //
 // Measured: those 48 sequences (406 MB, e4m3, 8 heads of 128, groups of 4) 71 us,
 // 5.7 TB/s, 0.87 of the measured copy rate; 102960 tokens of 40 heads in int4 (593 MB)
-// 143 us, 4.1 TB/s, 0.64, bound by the integer pipe and issue slots (760 instructions
-// a 32-token tile, of which 160 unpack nibbles); one sequence of 999 tokens 10.2 us.
+// 145 us, 4.1 TB/s, 0.62, bound by issue slots and the integer pipe (800 instructions
+// a 32-token tile, of which 160 unpack nibbles; issue slots 64 % busy, integer pipe 51 %,
+// DRAM 47 %); one sequence of 999 tokens 10.4 us, of 16000 18.7 us.
+//
+// Registers: 168 a thread with three CTAs an SM, 128 with four.  Blocks of 8 rows spill nothing
+// but 16 bytes in int4 with d = 128; every kernel with blocks of 16 rows spills (8 to 204 bytes
+// stored, 12 to 224 loaded, most with d = 128 and fp16 inputs), once a tile: two CTAs an SM instead
+// would leave too few loads in flight.
 //
 // Codes go into fp16 exactly: e4m3 and int8 values as they are, int4 values
 // times the group's e4m3 factor (7 significant bits).  The per-token scales
@@ -53,12 +59,12 @@ constexpr int kMaxCtas = 4;       // CTAs per SM at most (Geo::CTAS)
 constexpr int kItem = 8;          // steps counted for an item besides its tiles
 constexpr int kMinTail = 4;       // tiles that are worth cutting off
 constexpr int kMinHead = kItem + kMinTail;
-constexpr float kAhead = 4.f;     // a row's reference is put this far (log2) above its largest score, and moves
-                                  // when a score passes it by as much: weights are at most 2^4, so that their
-                                  // products with V's scales (below 2^121) stay in fp32's range
-constexpr int kUpMax = 253;       // exponent field of a row's power of two at most (2^126)
-constexpr int kUpTo = 127 + 9;    // its largest product is put into [2^9, 2^10) ...
-constexpr float kUpLimit = 32768.f;  // ... and moved when it comes to this
+// A row's softmax reference is put kAhead (log2) above its largest score and moves when a score
+// passes it by as much: weights are at most 2^4, so that their products with V's scales (below
+// 2^121) stay in fp32's range.  The row's power of two puts its largest product into [2^9, 2^10)
+// (kUpTo: 127 + 9) and moves when one comes to kUpLimit = 2^15; its exponent field is kUpMax at most.
+constexpr float kAhead = 4.f, kUpLimit = 32768.f;
+constexpr int kUpTo = 127 + 9, kUpMax = 253;
 constexpr float kNegInf = -INFINITY;
 
 struct KvqParams {

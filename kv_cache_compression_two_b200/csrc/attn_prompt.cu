@@ -37,10 +37,12 @@
 // the FMA pipe (the same to 10 % slower), one thread a row with the scores in registers
 // (spills), spinning waits, one pass over the scores with a late correction (spills).
 //
-// Measured (bf16, d = 128): 8192 causal tokens, 32 heads on 8, 450 us, 1220 TFLOP/s (0.72
-// of the measured burst peak, 0.86 of the sustained one); 4680 queries over 32760 keys, 12
-// heads, 742 us alone, 1270 TFLOP/s; six prompts of 545 to 2815 tokens 157 us, 890
-// TFLOP/s; 24 prompts of 1 to 300 tokens (d = 64) 14.1 us.
+// Measured (bf16, d = 128), in a graph of a few calls / in long runs at the power cap: 8192
+// causal tokens, 32 heads on 8, 450 to 463 / 535 us, 1190 to 1220 / 1030 TFLOP/s (0.71 to 0.72 of
+// the measured burst peak / 0.73 of the sustained one); 4680 queries over 32760 keys, 12 heads, 742
+// to 843 / 875 us, 1270 to 1120 / 1080 TFLOP/s; six prompts of 545 to 2815 tokens 158 / 184 us, 890 /
+// 760 TFLOP/s; 24 prompts of 1 to 300 tokens (d = 64) 13.7 us.  8192 tokens in fp16: 530 us; with
+// d = 64 484 (bf16) and 435 us (fp16), 565 and 630 TFLOP/s: half the products for as many exponentials.
 //
 // Ordering (MMAs of one thread execute in order; a commit fires when all
 // earlier ones have completed): S_{j+1} is issued after PV_j of the same tile,

@@ -1,10 +1,11 @@
 // kvq.cu -- writing rows into the quantised paged cache and reading them back.
 //
-// Both are one pass over their bytes.  Reading is bound by memory: 184 MB (23400 tokens
-// of 12 heads, int4) in 38 us, 4.9 TB/s, 0.75 of the measured copy rate (it writes four
-// bytes for each one read).  Writing is bound by its arithmetic, about 20 instructions
-// a lane and value with the reductions: 12 us for 4680 tokens of 12 heads (37 MB, 3.1 TB/s;
-// 25 us with a division a value).  A decoding step's few rows are bound by the launch.
+// Both are one pass over their bytes.  Reading 23400 tokens of 12 heads takes 36.5 us in
+// e4m3, 37 in int8 (218 MB, 5.9 TB/s, 0.9 of the measured copy rate) and 40 us in int4 (184 MB,
+// 4.6 TB/s, 0.7): there the issue slots (75 % busy) and the integer pipe (71 %) bind, 474
+// instructions a warp for 1024 values.  Writing as many is bound by its arithmetic: 46 us in
+// int8, 51 in e4m3, 55 in int4 (662 instructions a warp for 1024 values, issue slots 76 % busy;
+// 4680 tokens 10.7, 12.2 and 12.3 us).  A decoding step's few rows are bound by the launch.
 // A row (one token of one head) is handled by d / 16 lanes, 16 values each: with 8 a
 // lane the reductions and reciprocals of a row cost as much as its values.  A warp takes
 // one token and up to kHeads heads of K and of V, whose loads are all issued before the
@@ -50,7 +51,8 @@ __device__ __forceinline__ float2 e4m3x2_to_float(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// 1 / b to about 2^-23, for b in [2^-120, 2^121].
+// 1 / b to about 2^-23, for b in [2^-120, 2^125]: the largest is int4's amax / 512 * g / 8 =
+// 0.11 amax of the largest bf16 rows, and leaves one power of two to where the result is flushed.
 __device__ __forceinline__ float reciprocal(float b) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
@@ -217,8 +219,8 @@ template <>
 __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) { return pack_bf16x2(lo, hi); }
 
 // Reading: a warp takes one token of up to four heads, all loads first.  Eight values a
-// lane here, so that a warp's stores are whole lines (sixteen a lane: 43 us instead of 38 for
-// 23400 tokens of 12 heads in int4; two or four tokens a warp, or streaming stores: no change).
+// lane here, so that a warp's stores are whole lines (sixteen a lane: 43 us instead of 38 to 40
+// for 23400 tokens of 12 heads in int4; two or four tokens a warp, or streaming stores: no change).
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads) kvq_read_kernel(RowParams P) {
   constexpr int W = D / 8;

@@ -3,7 +3,10 @@ import numpy as np
 import pytest
 import torch
 
-from seq_bounds import random_rows, run_cached
+import kv_cache_compression_two_b200 as ispa
+from oracle import seq_oracle as so
+from seq_bounds import ints, random_rows, run_cached
+from seq_helpers import check_attention, f64, rand16
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +56,25 @@ def test_a_few_rows_of_padding_change_no_bit(fmt, d, G):
     more = torch.cat([q, torch.full((3, G, d), float("nan"), dtype=q.dtype)])
     o2, lse2 = run_cached(np.random.default_rng(0), fmt, more, k, v, lens, [1] * 8)
     assert torch.equal(o, o2[:8]) and torch.equal(lse, lse2[:8]) and torch.all(o2[8:] == 7.0) and torch.all(lse2[8:] == 7.0)
+
+
+def test_prompts_beyond_four_gib():
+    """Offsets past 32 bits in q, o, k and v: the last sequence of a call of 4.9 and 4.5 GB tensors."""
+    rng = np.random.default_rng(92)
+    H, H_kv, d, many_q, many_k, n = 32, 8, 128, 600_000, 2_200_000, 300
+    q = torch.zeros(many_q + n, H, d, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(many_k + n, H_kv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert 2 * k[:many_k].numel() > 2 ** 32 and q[:many_q].numel() > 2 ** 31
+    hq, hk, hv = (rand16(rng, (n, h, d), torch.bfloat16) for h in (H, H_kv, H_kv))
+    q[many_q:], k[many_k:], v[many_k:] = hq.cuda(), hk.cuda(), hv.cuda()
+    v[:many_k] = 0.5
+    a = ispa.attn_seq_desc(3, H, H_kv, d, ispa.ISPA_BF16, ispa.ISPA_BF16)
+    o, lse = torch.full_like(q, 7.0), torch.full((many_q + n, H), 7.0, device="cuda")
+    ws = torch.empty(ispa.ispa_attn_prompt_workspace_bytes(a), dtype=torch.uint8, device="cuda")
+    # one query over 2.2 million keys, many queries without a key, then the sequence that is looked at
+    ispa.ispa_attn_prompt(a, q, k, v, ints([0, 1, many_q, many_q + n]), ints([0, many_k, many_k, many_k + n]), o, lse, workspace=ws)
+    ispa.ispa_check_device_error()
+    check_attention(o[many_q:], lse[many_q:], so.attention(f64(hq), f64(hk), f64(hv), True), 2.0 ** -8, d, n, np.abs(f64(hv)).max())
+    assert torch.all(o[1:many_q] == 0) and torch.all(torch.isneginf(lse[1:many_q]))
+    # equal scores: the mean of equal values, of weights that are exact
+    assert torch.all(o[0] == 0.5) and torch.all((lse[0] - np.log(many_k)).abs() < many_k * 2.0 ** -23)
