@@ -654,7 +654,7 @@ typedef struct {
  * [T, H, d], its keys the first seq_lens[b] tokens of its cache; with causal,
  * the queries are its last tokens (already written).  Any number of query
  * tokens is taken; the cache is read once per 8 rows of tokens * (H / H_kv) when
- * the call has no more than 16 to a sequence on the average (T * (H / H_kv) / B,
+ * the call has no more than 11 to a sequence on the average (T * (H / H_kv) / B,
  * rows of padding counted), else once per 16.
  *   o    [T, H, d] out_dtype, lse [T, H] fp32 or NULL.  A query that sees no
  *        key gives O = 0, lse = -inf; one that holds a NaN gives NaN in its own

@@ -15,7 +15,7 @@
 // is looked up one tile ahead; tokens past the length are filled with zeros, so
 // nothing that lies there matters).  No barrier is needed until the states are merged
 // at the end of the CTA's stretch of an item (seq.cuh); parts of an item that other
-// CTAs hold are merged by kvq_merge_kernel.  Three or four CTAs share an SM, so that
+// CTAs hold are merged by kvq_merge_kernel.  Two to four CTAs share an SM, so that
 // an item's start and end in one are covered by the others: 48 sequences of 200 to
 // 16000 tokens took 137 us with one CTA of 12 warps an SM and items counted by their
 // tiles, 78 us (71 now) with four warps and an item's fixed cost counted.
@@ -26,10 +26,7 @@
 // a 32-token tile, of which 160 unpack nibbles; issue slots 64 % busy, integer pipe 51 %,
 // DRAM 47 %); one sequence of 999 tokens 10.4 us, of 16000 18.7 us.
 //
-// Registers: 168 a thread with three CTAs an SM, 128 with four.  Blocks of 8 rows spill nothing
-// but 16 bytes in int4 with d = 128; every kernel with blocks of 16 rows spills (8 to 204 bytes
-// stored, 12 to 224 loaded, most with d = 128 and fp16 inputs), once a tile: two CTAs an SM instead
-// would leave too few loads in flight.
+// No kernel spills but int4's with d = 128, fp16 inputs and blocks of 8 rows (16 bytes a thread).
 //
 // Codes go into fp16 exactly: e4m3 and int8 values as they are, int4 values
 // times the group's e4m3 factor (7 significant bits).  The per-token scales
@@ -113,10 +110,13 @@ struct Geo {
   static constexpr int CODE = kTile * ROW, SCALE = kTile * REC;
   static constexpr int STAGE = 2 * (CODE + SCALE);
   static constexpr int ROWS = 8 * NR;
-  // CTAs of four warps, as many to an SM as registers (168 a thread with 12 warps, 128 with
-  // 16) and shared memory hold.
+  // CTAs of four warps, as many to an SM as shared memory and registers hold without spills (255 a
+  // thread with two CTAs, 168 with three, 128 with four).  Blocks of 16 rows with one CTA more
+  // spilled 8 to 224 bytes a thread: 16 sequences of 24 rows over 3000 to 9000 tokens, d = 128, took
+  // 50 (e4m3), 55 (int8) and 53 us (int4) instead of 45, 49 and 48, in fp16 62, 62 and 59 instead of 50,
+  // 55 and 54; d = 64 34, 36 and 37 instead of 32, 34 and 35 (64 sequences: up to 2 % the other way).
   static constexpr int WARPS = 4;
-  static constexpr int CTAS = STAGE > 8192 || (D == 128 && NR == 2) ? 3 : 4;
+  static constexpr int CTAS = D == 128 && NR == 2 ? 2 : STAGE > 8192 || NR == 2 ? 3 : 4;
   static constexpr int QBYTES = (D / 16) * NR * 32 * 8;
   static constexpr int FIT = (233472 / CTAS - 2048 - QBYTES) / (WARPS * STAGE);
   static constexpr int STAGES = FIT < 4 ? FIT : 4;
@@ -956,20 +956,19 @@ ispa_status launch_rows(KvqParams P, cudaStream_t s) {
   return cuda_status(e, "kvq_merge launch");
 }
 
-// Row blocks of 8 up to 16 rows a sequence, else of 16, which read and unpack the cache half as
-// often.  The number is an average over the call, rows of padding counted (the arrays are on the
-// device), and the two sides lie close together around it: 16 sequences of 3000 to 9000 tokens, 4 K/V
-// heads, us with blocks of 8 / of 16:
-//   rows a sequence      8            9            16           32
-//   e4m3, d = 128    28.2 / 36.2  34.0 / 38.6  34.8 / 38.6  53.2 / 50.3
-//   int8, d = 128    29.9 / 38.2  38.9 / 39.9  39.6 / 40.3  63.1 / 54.6
-//   int4, d = 128    29.0 / 35.8  39.6 / 37.9  40.1 / 38.1  62.3 / 53.2
-//   e4m3, d = 64     23.0 / 26.5  26.6 / 27.5  27.3 / 27.1  40.5 / 35.2
-// (With the line at 8, one row of padding took a batch of 8 rows a sequence from the left column
-// to its right side.)
+// Row blocks of 8 when a sequence's rows fit one, else of 16, which read and unpack the cache half
+// as often.  The number of rows is an average over the call, rows of padding counted (the arrays
+// are on the device), so the line lies at 11: 8 rows and up to three of padding for eight sequences.
+// 16 sequences of 3000 to 9000 tokens, 4 K/V heads, us with blocks of 8 / of 16:
+//   rows a sequence      4            8            9            16           32
+//   e4m3, d = 128    27.0 / 30.0  28.0 / 31.9  34.0 / 32.9  35.0 / 32.9  53.2 / 45.7
+//   int8, d = 128    28.0 / 32.3  29.4 / 34.3  39.1 / 34.6  39.6 / 34.6  63.1 / 49.3
+//   int4, d = 128    29.0 / 31.7  29.4 / 33.3  39.6 / 33.8  40.1 / 33.3  62.6 / 49.2
+//   e4m3, d = 64     22.0 / 24.6  23.2 / 24.6  27.1 / 25.7  27.1 / 25.1  40.3 / 33.1
+// (With the line at 8, one row of padding took a batch of 8 rows a sequence to the right side.)
 template <int FMT, int D, typename T, typename TO>
 ispa_status launch_one(const KvqParams &P, cudaStream_t s) {
-  return (long long)P.G * P.T <= 16LL * P.B ? launch_rows<FMT, D, 1, T, TO>(P, s) : launch_rows<FMT, D, 2, T, TO>(P, s);
+  return (long long)P.G * P.T <= 11LL * P.B ? launch_rows<FMT, D, 1, T, TO>(P, s) : launch_rows<FMT, D, 2, T, TO>(P, s);
 }
 
 template <int FMT, int D>
