@@ -7,6 +7,11 @@ largest, and its token's values are at most s * (largest code) = the row's amax
 of V.  Over N keys that is N 2^-34 max_j(p_j amax_j): seq_helpers.check_attention
 takes it as N 2^-25 times the array that smallest_step() returns.  (fp16 inputs
 enter as two fp16 numbers, of which the second one has the same smallest step.)
+
+The allowance of 2^-18 max|v| a key that seq_helpers names for the cached attention
+(and that tests pass as max|v| * 2^7) has the wrong sign of exponent: it exceeds the
+whole output of a long cache, so that those tests pin O by short caches and long ones
+by the log-sum-exp alone.  The tests that use this file pin O at every length.
 """
 import numpy as np
 import torch
