@@ -695,6 +695,8 @@ ispa_status ispa_attn_kvq(const ispa_attn_seq_desc *desc, const ispa_kvq_desc *c
  *   fp16 with 11 down to 2^-21 of the query's largest, below it with an error of
  *   at most 2^-32 of that.
  *   workspace >= ispa_attn_prompt_workspace_bytes(desc), as for ispa_attn_kvq.
+ *   The same inputs give the same bits, which do not depend on the values of
+ *   other sequences.
  */
 size_t ispa_attn_prompt_workspace_bytes(const ispa_attn_seq_desc *desc);
 ispa_status ispa_attn_prompt(const ispa_attn_seq_desc *desc, int Tq, int Tk, const int *cu_q, const int *cu_k,

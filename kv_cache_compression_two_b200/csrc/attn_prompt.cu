@@ -731,7 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mt = fmaxf(mt, *theirs) * P.scale_log2;
         if (j == j0) {
           m_ref = mt == -INFINITY ? 0.f : mt - Ref<T>::behind;
-        } else if (__any_sync(0xffffffffu, mt > m_ref + Ref<T>::limit)) {
+        } else if (__any_sync(0xffffffffu, row_ok && mt > m_ref + Ref<T>::limit)) {
+          // (rows that are none hold what lies behind the sequence, or in shared memory behind TQ G rows:
+          // they must not move the others, whose roundings would depend on it)
           const float m_new = fmaxf(m_ref, mt - Ref<T>::behind);
           const float f = exp2_fast(m_ref - m_new);
           m_ref = m_new;
