@@ -874,11 +874,11 @@ __global__ void __launch_bounds__(kTile) prompt_merge_kernel(PromptParams P) {
   const long long out = (long long)(own.row + t) * P.H + own.head * P.G + head;
   const float inv = ll == 0.f ? 0.f : 1.f / ll;  // (a sum that is NaN stays so)
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    float y[8];
+  for (int v = 0; v < 2; ++v) {
+    float y[16];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) y[t] = x[8 * v + t] * inv;
-    store8(static_cast<TO *>(P.o) + out * D + c0 + v * 8, y);
+    for (int t = 0; t < 16; ++t) y[t] = x[16 * v + t] * inv;
+    store16(static_cast<TO *>(P.o) + out * D + c0 + v * 16, y, P.wide);
   }
   if (P.lse && c0 == 0) P.lse[out] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
 }

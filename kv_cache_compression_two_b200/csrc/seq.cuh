@@ -248,10 +248,17 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&x)[16], 
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
   store32b(p, w, wide);
 }
+// A prompt's output is a mean of fp16 values: where rounded weights (off by 2^-11) carry it past the
+// largest number of the type, it is that one and not infinity.  (NaN stays NaN.)
+__device__ __forceinline__ uint32_t pack_half2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ void store16(__half *p, const float (&x)[16], bool wide) {
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+  for (int i = 0; i < 8; ++i) w[i] = pack_half2_sat(x[2 * i], x[2 * i + 1]);
   store32b(p, w, wide);
 }
 

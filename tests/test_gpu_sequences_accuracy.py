@@ -120,3 +120,23 @@ def test_small_weights_of_a_prompt_add_up(d, first, n, nq, log2, causal):
     ispa.ispa_check_device_error()
     ref = so.attention(f64(q), f64(k), f64(v), causal)
     check_attention(o, lse, ref, 2.0 ** -11, d, n, f64(v).max() * 2.0 ** -7)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,nq", [(300, 1), (3000, 2)])
+def test_values_at_the_end_of_fp16_stay_finite(d, n, nq):
+    """One late key holds nearly all of the weight, which fp16 rounds up by almost 2^-11: O is still V's largest.
+
+    Weights are 2^7 for the first tile's largest and 2^12 * 1.0005 for the late key (fp16: 2^12 * (1 + 2^-10)),
+    so that the mean comes to 65504 (1 + 2^-11.1), above 65520, where rounding to fp16 gives infinity."""
+    q, k = torch.zeros(nq, 1, d, dtype=torch.float16), torch.zeros(n, 1, d, dtype=torch.float16)
+    q[:, :, 0], k[:, :, 0] = 2.0, -60.0
+    k[0, 0, 0], k[n - nq, 0, 0] = 0.0, 4.0
+    v = torch.full((n, 1, d), 65504.0, dtype=torch.float16)
+    v[:, :, 1::2] *= -1.0
+    scale = (5.0 + np.log2(1.0005)) * np.log(2.0) / 8.0
+    a = ispa.attn_seq_desc(1, 1, 1, d, ispa.ISPA_F16, ispa.ISPA_F16, False, scale)
+    o, ws = torch.empty_like(q, device="cuda"), torch.empty(ispa.ispa_attn_prompt_workspace_bytes(a), dtype=torch.uint8, device="cuda")
+    ispa.ispa_attn_prompt(a, q.cuda(), k.cuda(), v.cuda(), ints([0, nq]), ints([0, n]), o, None, workspace=ws)
+    ispa.ispa_check_device_error()
+    assert torch.equal(o.cpu(), v[:1].expand(nq, 1, d))

@@ -5,7 +5,7 @@ import torch
 
 import kv_cache_compression_two_b200 as ispa
 from oracle import seq_oracle as so
-from seq_bounds import ints, random_rows, run_cached
+from seq_bounds import CODE, ints, random_rows, run_cached
 from seq_helpers import check_attention, f64, rand16
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +78,26 @@ def test_prompts_beyond_four_gib():
     assert torch.all(o[1:many_q] == 0) and torch.all(torch.isneginf(lse[1:many_q]))
     # equal scores: the mean of equal values, of weights that are exact
     assert torch.all(o[0] == 0.5) and torch.all((lse[0] - np.log(many_k)).abs() < many_k * 2.0 ** -23)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
+def test_joined_prompts_at_every_alignment_allowed(out):
+    """O 16-byte but not 32-byte aligned, written by the merge of the parts: the same bits as an aligned one."""
+    rng = np.random.default_rng(93)
+    dtype = torch.float16 if out is torch.float16 else torch.bfloat16
+    q, k, v = (rand16(rng, s, dtype).cuda() for s in ((40, 2, 64), (9000, 1, 64), (9000, 1, 64)))
+    a = ispa.attn_seq_desc(1, 2, 1, 64, CODE[dtype], CODE[out])
+    ws = torch.empty(ispa.ispa_attn_prompt_workspace_bytes(a), dtype=torch.uint8, device="cuda")
+    got = []
+    for shift in (0, 16):
+        n = shift // torch.empty(0, dtype=out).element_size()
+        buf = torch.full((40 * 2 * 64 + 16,), 7.0, dtype=out, device="cuda")
+        o = buf[n:n + 40 * 2 * 64].view(40, 2, 64)
+        assert o.data_ptr() % 32 == shift
+        ispa.ispa_attn_prompt(a, q, k, v, ints([0, 40]), ints([0, 9000]), o, None, workspace=ws)
+        assert torch.all(buf[:n] == 7.0) and torch.all(buf[n + 40 * 2 * 64:] == 7.0)
+        got.append(o.clone())
+    assert torch.equal(*got)
+    check_attention(got[0], None, so.attention(f64(q), f64(k), f64(v), True), 2.0 ** -11 if dtype is torch.float16 else 2.0 ** -8,
+                    64, 9000, np.abs(f64(v)).max() * 2.0 ** -7)
+    ispa.ispa_check_device_error()
