@@ -693,7 +693,8 @@ ispa_status ispa_attn_kvq(const ispa_attn_seq_desc *desc, const ispa_kvq_desc *c
  *   tcgen05 tensor cores, fp32 accumulation and statistics; the softmax
  *   weights enter the second product in in_dtype: bf16 with 8 significant bits;
  *   fp16 with 11 down to 2^-21 of the query's largest, below it with an error of
- *   at most 2^-32 of that.
+ *   at most 2^-32 of that; an fp16 output that the weights' rounding would carry
+ *   past 65504 is 65504.
  *   workspace >= ispa_attn_prompt_workspace_bytes(desc), as for ispa_attn_kvq.
  *   The same inputs give the same bits, which do not depend on the values of
  *   other sequences.
